@@ -483,6 +483,39 @@ moe_status moe_backward(const moe_problem *p, const moe_weights *w, const void *
                         const int64_t *selected_experts, moe_grads *g, void *ws, size_t ws_bytes,
                         moe_stream_t stream);
 
+/* ---- Token rows sorted by expert and back -------------------------------------
+ * The row movement around experts of the caller's own, with its gradients.
+ * The plan is the one moe_dispatch (or moe_dispatch_slots) returns for the
+ * same problem: pair_pos [T*k] and offsets [E+1] int32. A pair with pair_pos
+ * outside [0, T*k) has no row. dtype is the problem's; only T, H, E, k and
+ * dtype are used. Every sum runs in fp32 in slot order (d_routing_weights: in
+ * a fixed order) and each result is rounded once: results are deterministic.
+ * No workspace; async on `stream`; the calls can be captured.
+ *   moe_permute_rows: x_perm[pair_pos[t*k+j]] = x[t] (x [T,H] and x_perm
+ *     [T*k,H] in the problem dtype); rows at or past offsets[E] are zeros.
+ *   moe_permute_rows_backward: dx[t] = sum_j dx_perm[pair_pos[t*k+j]], both in
+ *     the problem dtype.
+ *   moe_unpermute_rows: out[t] = round(sum_j w[t,j] * y_perm[pair_pos[t*k+j]]
+ *     + shared_out[t]). y_perm [T*k,H] is fp32 or has the problem dtype
+ *     (y_dtype, a moe_dtype); routing_weights [T,k] fp32, NULL for 1;
+ *     shared_out [T,H] fp32 or NULL; out [T,H] in the problem dtype. A pair
+ *     without a row adds nothing, whatever its weight.
+ *   moe_unpermute_rows_backward: dy_perm[pair_pos[t*k+j]] = w[t,j] * dout[t]
+ *     in y_dtype (rows at or past offsets[E] are zeros), and
+ *     d_routing_weights[t,j] = <dout[t], y_perm[pair_pos[t*k+j]]> fp32 (0 for
+ *     a pair without a row). Either result may be NULL, not both; y_perm is
+ *     read for the second only, offsets for the first only. shared_out's
+ *     gradient is dout itself. */
+moe_status moe_permute_rows(const moe_problem *p, const void *x, const int32_t *pair_pos, const int32_t *offsets,
+                            void *x_perm, moe_stream_t stream);
+moe_status moe_permute_rows_backward(const moe_problem *p, const void *dx_perm, const int32_t *pair_pos, void *dx,
+                                     moe_stream_t stream);
+moe_status moe_unpermute_rows(const moe_problem *p, int32_t y_dtype, const void *y_perm, const int32_t *pair_pos,
+                              const float *routing_weights, const float *shared_out, void *out, moe_stream_t stream);
+moe_status moe_unpermute_rows_backward(const moe_problem *p, int32_t y_dtype, const void *dout, const void *y_perm,
+                                       const int32_t *pair_pos, const int32_t *offsets, const float *routing_weights,
+                                       void *dy_perm, float *d_routing_weights, moe_stream_t stream);
+
 /* Static description of a status code. */
 const char *moe_status_string(moe_status s);
 

@@ -12,6 +12,7 @@ Build the library with ``python -m sparse_top_mixture_b200.build``.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -101,6 +102,10 @@ SIGNATURES = {
     "moe_tp_scatter": (ctypes.c_int, [_PP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP]),
     "moe_tp_gather": (ctypes.c_int, [_PP, ctypes.c_int32, ctypes.c_int32, _VP, _VP, _VP]),
     "moe_tp_wait": (ctypes.c_int, [_PP, ctypes.c_int32, _VP, ctypes.c_int32, ctypes.c_int64, _VP, _VP]),
+    "moe_permute_rows": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_permute_rows_backward": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP]),
+    "moe_unpermute_rows": (ctypes.c_int, [_PP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_unpermute_rows_backward": (ctypes.c_int, [_PP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -162,6 +167,11 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(device=None) -> int:
     return torch.cuda.current_stream(device).cuda_stream
+
+
+def _on(device: torch.device):
+    """Makes ``device`` the current one for a launch on its stream."""
+    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
 
 def _req(t: torch.Tensor, name: str, shape: Sequence[int], dtype: torch.dtype) -> None:
@@ -628,3 +638,7 @@ class HostPipeline:
     def synchronize(self) -> None:
         for slot in self.slots:
             slot["stream"].synchronize()
+
+
+from .rows import (permute_rows, permute_rows_backward, unpermute_rows,  # noqa: E402
+                   unpermute_rows_backward)

@@ -1,0 +1,173 @@
+"""Token rows sorted by expert and back in token order, with their gradients.
+
+For experts of the caller's own between the library's dispatch and its
+weighted return: ``permute_rows`` copies each token's row to its k segment
+slots, ``unpermute_rows`` sums a token's k rows with the routing weights. Both
+take part in autograd (in ``x``; in ``y_perm``, ``routing_weights`` and
+``shared_out``); ``permute_rows_backward`` and ``unpermute_rows_backward`` are
+their gradients as plain calls. The plan is what ``dispatch`` or
+``dispatch_slots`` returned for the same problem.
+
+    plan = stm.dispatch(p, selected_experts)
+    rows = stm.permute_rows(p, x, plan)                 # [T*k, H], by expert
+    y = my_experts(rows, plan["offsets"])
+    out = stm.unpermute_rows(p, y, plan, routing_weights)
+"""
+
+from __future__ import annotations
+
+import ctypes
+from typing import Dict, Optional, Tuple
+
+import torch
+
+from . import DTYPES, Problem, _check, _on, _ptr, _req, _stream, lib
+
+
+def _plan(p: Problem, plan: Dict[str, torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
+    pair_pos, offsets = plan["pair_pos"], plan["offsets"]
+    _req(pair_pos, "pair_pos", (p.T * p.k,), torch.int32)
+    _req(offsets, "offsets", (p.E + 1,), torch.int32)
+    return pair_pos, offsets
+
+
+def _same_device(dev: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _y_dtype(p: Problem, y_perm) -> int:
+    if isinstance(y_perm, torch.Tensor) and y_perm.dtype == torch.float32:
+        return DTYPES["f32"]
+    return DTYPES[p.dtype]
+
+
+def _req_y(p: Problem, y_perm) -> int:
+    yd = _y_dtype(p, y_perm)
+    _req(y_perm, "y_perm", (p.T * p.k, p.H), torch.float32 if yd == DTYPES["f32"] else p.torch_dtype)
+    return yd
+
+
+def _permute(p: Problem, x, pair_pos, offsets):
+    out = torch.empty(p.T * p.k, p.H, dtype=p.torch_dtype, device=x.device)
+    with _on(x.device):
+        _check(lib().moe_permute_rows(ctypes.byref(p.c()), _ptr(x), _ptr(pair_pos), _ptr(offsets), _ptr(out),
+                                      _stream(x.device)))
+    return out
+
+
+def _permute_backward(p: Problem, dx_perm, pair_pos):
+    dx = torch.empty(p.T, p.H, dtype=p.torch_dtype, device=dx_perm.device)
+    with _on(dx.device):
+        _check(lib().moe_permute_rows_backward(ctypes.byref(p.c()), _ptr(dx_perm), _ptr(pair_pos), _ptr(dx),
+                                               _stream(dx.device)))
+    return dx
+
+
+def _unpermute(p: Problem, yd: int, y_perm, pair_pos, routing_weights, shared_out):
+    out = torch.empty(p.T, p.H, dtype=p.torch_dtype, device=y_perm.device)
+    with _on(out.device):
+        _check(lib().moe_unpermute_rows(ctypes.byref(p.c()), yd, _ptr(y_perm), _ptr(pair_pos), _ptr(routing_weights),
+                                        _ptr(shared_out), _ptr(out), _stream(out.device)))
+    return out
+
+
+def _unpermute_backward(p: Problem, yd: int, dout, y_perm, pair_pos, offsets, routing_weights, rows: bool,
+                        weights: bool):
+    dev = dout.device
+    dy = torch.empty(p.T * p.k, p.H, dtype=torch.float32 if yd == DTYPES["f32"] else p.torch_dtype,
+                     device=dev) if rows else None
+    dw = torch.empty(p.T, p.k, dtype=torch.float32, device=dev) if weights else None
+    if rows or weights:
+        with _on(dev):
+            _check(lib().moe_unpermute_rows_backward(ctypes.byref(p.c()), yd, _ptr(dout), _ptr(y_perm),
+                                                     _ptr(pair_pos), _ptr(offsets), _ptr(routing_weights), _ptr(dy),
+                                                     _ptr(dw), _stream(dev)))
+    return dy, dw
+
+
+class _PermuteRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, pair_pos, offsets):
+        ctx.p = p
+        ctx.save_for_backward(pair_pos)
+        return _permute(p, x, pair_pos, offsets)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dx_perm):
+        (pair_pos,) = ctx.saved_tensors
+        return _permute_backward(ctx.p, dx_perm.contiguous(), pair_pos), None, None, None
+
+
+class _UnpermuteRows(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets):
+        ctx.p, ctx.yd = p, yd
+        needs_y = ctx.needs_input_grad[1]  # the rows themselves enter the weights' gradient only
+        ctx.save_for_backward(y_perm if needs_y else None, routing_weights, pair_pos, offsets)
+        return _unpermute(p, yd, y_perm, pair_pos, routing_weights, shared_out)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dout):
+        y_perm, routing_weights, pair_pos, offsets = ctx.saved_tensors
+        dout = dout.contiguous()
+        rows, weights, shared = ctx.needs_input_grad[:3]
+        dy, dw = _unpermute_backward(ctx.p, ctx.yd, dout, y_perm, pair_pos, offsets, routing_weights, rows, weights)
+        return dy, dw, dout.float() if shared else None, None, None, None, None
+
+
+def permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]):
+    """x_perm [T*k, H]: each token's row of x [T, H] copied to its k sorted
+    positions. Rows past the last segment are zeros. Differentiable in x."""
+    _req(x, "x", (p.T, p.H), p.torch_dtype)
+    pair_pos, offsets = _plan(p, plan)
+    _same_device(x.device, pair_pos=pair_pos, offsets=offsets)
+    if torch.is_grad_enabled() and x.requires_grad:
+        return _PermuteRows.apply(x, p, pair_pos, offsets)
+    return _permute(p, x, pair_pos, offsets)
+
+
+def permute_rows_backward(p: Problem, dx_perm, plan: Dict[str, torch.Tensor]):
+    """dx [T, H] from dx_perm [T*k, H] (both in the problem's dtype): the sum
+    of each token's k rows, in fp32, rounded once."""
+    _req(dx_perm, "dx_perm", (p.T * p.k, p.H), p.torch_dtype)
+    pair_pos, _ = _plan(p, plan)
+    _same_device(dx_perm.device, pair_pos=pair_pos)
+    return _permute_backward(p, dx_perm, pair_pos)
+
+
+def unpermute_rows(p: Problem, y_perm, plan: Dict[str, torch.Tensor], routing_weights=None, shared_out=None):
+    """out [T, H]: sum over each token's slots of routing_weights [T, k] (fp32;
+    1 when None) times its row of y_perm [T*k, H] (fp32 or the problem's
+    dtype), plus shared_out [T, H] fp32 when given; summed in fp32, rounded
+    once to the problem's dtype. A slot without a row adds nothing.
+    Differentiable in y_perm, routing_weights and shared_out."""
+    yd = _req_y(p, y_perm)
+    pair_pos, offsets = _plan(p, plan)
+    if routing_weights is not None:
+        _req(routing_weights, "routing_weights", (p.T, p.k), torch.float32)
+    if shared_out is not None:
+        _req(shared_out, "shared_out", (p.T, p.H), torch.float32)
+    _same_device(y_perm.device, pair_pos=pair_pos, offsets=offsets, routing_weights=routing_weights,
+                 shared_out=shared_out)
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
+                                       for t in (y_perm, routing_weights, shared_out)):
+        return _UnpermuteRows.apply(y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets)
+    return _unpermute(p, yd, y_perm, pair_pos, routing_weights, shared_out)
+
+
+def unpermute_rows_backward(p: Problem, dout, y_perm, plan: Dict[str, torch.Tensor], routing_weights=None):
+    """(dy_perm [T*k, H] in y_perm's dtype, d_routing_weights [T, k] fp32) for
+    dout [T, H]: each row's gradient is its weight times dout (rows past the
+    last segment are zeros), each weight's the product of dout and its row (0
+    for a slot without a row)."""
+    _req(dout, "dout", (p.T, p.H), p.torch_dtype)
+    yd = _req_y(p, y_perm)
+    pair_pos, offsets = _plan(p, plan)
+    if routing_weights is not None:
+        _req(routing_weights, "routing_weights", (p.T, p.k), torch.float32)
+    _same_device(dout.device, y_perm=y_perm, pair_pos=pair_pos, offsets=offsets, routing_weights=routing_weights)
+    return _unpermute_backward(p, yd, dout, y_perm, pair_pos, offsets, routing_weights, True, True)

@@ -1,0 +1,57 @@
+"""Host-side validation of the row movement's C entry points (no GPU: only
+calls that return before any CUDA work)."""
+
+import ctypes
+
+import pytest
+
+import sparse_top_mixture_b200 as stm
+
+
+def _p(**kw):
+    base = dict(T=64, H=256, E=8, k=2, I=128, dtype="bf16")
+    base.update(kw)
+    return ctypes.byref(stm.Problem(**base).c())
+
+
+A = 16  # an aligned, never followed address
+
+
+def test_permute_rows_validates():
+    L = stm.lib()
+    assert L.moe_permute_rows(None, A, A, A, A, None) == 1
+    for args in ((None, A, A, A), (A, None, A, A), (A, A, None, A), (A, A, A, None), (8, A, A, A), (A, A, A, 24)):
+        assert L.moe_permute_rows(_p(), *args, None) == 1
+    assert L.moe_permute_rows(_p(k=9), A, A, A, A, None) == 1
+    assert L.moe_permute_rows(_p(H=12), A, A, A, A, None) == 1
+    assert L.moe_permute_rows(_p(T=0), None, None, None, None, None) == 0
+    assert L.moe_permute_rows_backward(None, A, A, A, None) == 1
+    assert L.moe_permute_rows_backward(_p(), A, A, 8, None) == 1
+    assert L.moe_permute_rows_backward(_p(T=0), None, None, None, None) == 0
+
+
+@pytest.mark.parametrize("dtype,y_dtype,ok", [("bf16", 0, True), ("bf16", 1, True), ("f32", 0, True),
+                                              ("f32", 1, False), ("bf16", 2, False), ("bf16", -1, False)])
+def test_row_types(dtype, y_dtype, ok):
+    L = stm.lib()
+    want = 0 if ok else 1
+    assert L.moe_unpermute_rows(_p(T=0, dtype=dtype), y_dtype, None, None, None, None, None, None) == want
+    assert L.moe_unpermute_rows_backward(_p(T=0, dtype=dtype), y_dtype, None, None, None, None, None, None, None,
+                                         None) == want
+
+
+def test_unpermute_rows_validates():
+    L = stm.lib()
+    for args in ((None, A, A, A, A), (A, None, A, A, A), (A, A, A, A, None), (A, A, 8, A, A), (A, A, A, 8, A)):
+        assert L.moe_unpermute_rows(_p(), 1, *args, None) == 1
+
+
+def test_unpermute_rows_backward_validates():
+    L = stm.lib()
+    # dout, y_perm, pair_pos, offsets, routing_weights, dy_perm, d_routing_weights
+    bad = [(None, A, A, A, A, A, A), (A, A, None, A, A, A, A), (A, A, A, A, 8, A, A), (A, A, A, A, A, 8, A),
+           (A, A, A, A, A, A, 8), (A, A, A, A, A, None, None),  # nothing asked for
+           (A, None, A, A, A, A, A),   # the weights' gradient needs the rows
+           (A, A, A, None, A, A, A)]   # the rows' gradient needs the offsets
+    for args in bad:
+        assert L.moe_unpermute_rows_backward(_p(), 1, *args, None) == 1
