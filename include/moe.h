@@ -516,6 +516,52 @@ moe_status moe_unpermute_rows_backward(const moe_problem *p, int32_t y_dtype, co
                                        const int32_t *pair_pos, const int32_t *offsets, const float *routing_weights,
                                        void *dy_perm, float *d_routing_weights, moe_stream_t stream);
 
+/* ---- Microscaled 4-bit floating point -----------------------------------------
+ * Rows of K values (K a multiple of 32) as K/2 data bytes and
+ * S(K) = 16 * ceil(K / 512) scale bytes. Data: e2m1 codes (0, 0.5, 1, 1.5, 2,
+ * 3, 4, 6, and with bit 3 set their negatives), the value of even index in a
+ * byte's low half. Scales: byte b stands for 2^(b - 127) and 255 for NaN, one
+ * for every 32 values; the bytes past K/32 are padding, written as zeros and
+ * never used. Quantisation: b = max(0, floor(log2 m) - 2 + 127) for the
+ * block's largest magnitude m, each value times 2^(127 - b) rounded to the
+ * nearest code, ties to the even one, beyond 6 to 6; a block with an infinity
+ * or a NaN gets b = 255 and code 0. The power-of-two products are exact, so a
+ * given block has one result.
+ * Sizes are below 2^31; async on `stream`; the calls can be captured.
+ *   moe_mx4_quantize: x [rows, K] (dtype: a moe_dtype) to data and scale.
+ *   moe_mx4_dequantize: data and scale to out [rows, K] (dtype), code times
+ *     2^(b - 127), exact in both types unless the value underflows or
+ *     overflows them.
+ *   moe_mx4_permute_rows: as moe_permute_rows followed by moe_mx4_quantize,
+ *     each token quantised once: x [T,H] in the problem dtype, H a multiple of
+ *     32, data [T*k, H/2], scale [T*k, S(H)]; rows at or past offsets[E] are
+ *     zeros.
+ *   moe_mx4_grouped_matmul: out[p,n] = sum_i A[p,i] W[e,n,i] for the rows p of
+ *     each segment e of offsets [E+1]; A [rows, K] and W [E, N, K] in 4 bits,
+ *     N a multiple of 8, out [rows, N] fp32 or bf16 (out_dtype), accumulated in
+ *     fp32 and rounded once.
+ *   moe_mx4_grouped_gate_up: h[p,n] = silu(A[p] . W[e,n]) * (A[p] . W[e,I+n])
+ *     for W [E, 2I, H] in 4 bits (gate rows first), I a multiple of 32, rounded
+ *     to bf16: into h [rows, I] bf16 when h_scale is NULL; else that bf16 value
+ *     quantised, into h [rows, I/2] data bytes and h_scale [rows, S(I)], the
+ *     same bits as moe_mx4_quantize of the bf16 result.
+ *   The two products write the rows of the segments only, read only experts
+ *   that have rows, 1 <= E <= 256, and need no workspace: ws is a workspace
+ *   (its 256-byte header) for the error bits, or NULL. A malformed offsets
+ *   table raises MOE_DEVERR_BAD_EXPERT_ID there and computes nothing. */
+moe_status moe_mx4_quantize(int64_t rows, int64_t K, int32_t dtype, const void *x, void *data, void *scale,
+                            moe_stream_t stream);
+moe_status moe_mx4_dequantize(int64_t rows, int64_t K, int32_t dtype, const void *data, const void *scale, void *out,
+                              moe_stream_t stream);
+moe_status moe_mx4_permute_rows(const moe_problem *p, const void *x, const int32_t *pair_pos, const int32_t *offsets,
+                                void *data, void *scale, moe_stream_t stream);
+moe_status moe_mx4_grouped_matmul(int64_t rows, int64_t E, int64_t N, int64_t K, int32_t out_dtype,
+                                  const void *a_data, const void *a_scale, const int32_t *offsets, const void *w_data,
+                                  const void *w_scale, void *out, void *ws, moe_stream_t stream);
+moe_status moe_mx4_grouped_gate_up(int64_t rows, int64_t E, int64_t I, int64_t H, const void *a_data,
+                                   const void *a_scale, const int32_t *offsets, const void *w_data,
+                                   const void *w_scale, void *h, void *h_scale, void *ws, moe_stream_t stream);
+
 /* Static description of a status code. */
 const char *moe_status_string(moe_status s);
 

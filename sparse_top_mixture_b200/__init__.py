@@ -106,6 +106,11 @@ SIGNATURES = {
     "moe_permute_rows_backward": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP]),
     "moe_unpermute_rows": (ctypes.c_int, [_PP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP]),
     "moe_unpermute_rows_backward": (ctypes.c_int, [_PP, ctypes.c_int32, _VP, _VP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_mx4_quantize": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_int32, _VP, _VP, _VP, _VP]),
+    "moe_mx4_dequantize": (ctypes.c_int, [ctypes.c_int64] * 2 + [ctypes.c_int32, _VP, _VP, _VP, _VP]),
+    "moe_mx4_permute_rows": (ctypes.c_int, [_PP, _VP, _VP, _VP, _VP, _VP, _VP]),
+    "moe_mx4_grouped_matmul": (ctypes.c_int, [ctypes.c_int64] * 4 + [ctypes.c_int32] + [_VP] * 8),
+    "moe_mx4_grouped_gate_up": (ctypes.c_int, [ctypes.c_int64] * 4 + [_VP] * 9),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -605,7 +610,7 @@ class HostPipeline:
         self.moe = moe
         self.slots = []
         for i in range(depth):
-            m = moe if i == 0 else SparseMoE(p, moe.w, moe.device, overlap_shared=moe.aux is not None)
+            m = moe if i == 0 else type(moe)(p, moe.w, moe.device, overlap_shared=moe.aux is not None)
             slot = {
                 "moe": m,
                 "stream": torch.cuda.Stream(moe.device),
@@ -642,3 +647,5 @@ class HostPipeline:
 
 from .rows import (permute_rows, permute_rows_backward, unpermute_rows,  # noqa: E402
                    unpermute_rows_backward)
+from .mx4 import (Mx4, Mx4SparseMoE, mx4_dequantize, mx4_grouped_gate_up,  # noqa: E402
+                  mx4_grouped_matmul, mx4_permute_rows, mx4_quantize)

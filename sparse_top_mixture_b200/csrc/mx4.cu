@@ -1,0 +1,226 @@
+// Quantisation to microscaled 4-bit floating point and back (the format and
+// the rounding are in mx4.cuh), in the rows' own order or straight into the
+// dispatch's sorted order.
+//
+// Bound by memory: bf16 rows are read once (2 bytes a value) and written once
+// (17/32 of a byte). A warp takes 1024 consecutive values of one row, eight to
+// a lane and pass: four lanes share a block of 32, so the block's largest
+// magnitude takes two shuffles, every load is 16 bytes beside its neighbour's
+// and every store of a warp 128 bytes. All four passes' loads are issued before
+// the first is used.
+#include <cuda_runtime.h>
+
+#include "kernels.h"
+#include "moe.h"
+#include "mx4.cuh"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace stm {
+namespace {
+
+using namespace mx4;
+
+constexpr int QTHREADS = 256;
+constexpr int kPasses = 4;
+constexpr int kChunk = kPasses * 256;  // values per warp
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float* f) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  } else {
+    unpack16_bf16(__ldcs(reinterpret_cast<const uint4*>(p)), f);
+  }
+}
+
+// SORTED: row t's codes go to the rows pair_pos[t*k + j] of `data` and
+// `scale`, and the rows at or past offsets[E] are zeroed; else to row t.
+template <typename T, bool SORTED>
+__global__ void __launch_bounds__(QTHREADS) quantize_kernel(const T* __restrict__ x, int64_t rows, int K,
+                                                            uint32_t* __restrict__ data, uint8_t* __restrict__ scale,
+                                                            int pitch, int chunks,
+                                                            const int32_t* __restrict__ pair_pos,
+                                                            const int32_t* __restrict__ offsets, int k, int E) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp0 = (int64_t)blockIdx.x * (QTHREADS / 32) + (threadIdx.x >> 5);
+  const int64_t warps = (int64_t)gridDim.x * (QTHREADS / 32);
+  const int64_t P = rows * k;
+  for (int64_t it = warp0; it < rows * chunks; it += warps) {
+    const int64_t row = it / chunks;
+    const int c0 = (int)(it - row * chunks) * kChunk;
+    float f[kPasses][8];
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      const int col = c0 + u * 256 + lane * 8;
+      if (col < K) {
+        load8(x + row * K + col, f[u]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
+      }
+    }
+    uint32_t code[kPasses], b[kPasses];
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[u][i]) & 0x7fffffffu);
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      b[u] = scale_byte(m);
+      const float inv = inverse_scale(b[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[u][i] *= inv;
+      code[u] = b[u] == kScaleNaN ? 0u : pack8(f[u]);
+    }
+    const int pad0 = K / kBlock;  // the row's last chunk also writes the padding
+    auto store = [&](int64_t r) {
+      uint32_t* d = data + r * (K / 8);
+      uint8_t* s = scale + r * pitch;
+#pragma unroll
+      for (int u = 0; u < kPasses; ++u) {
+        const int col = c0 + u * 256 + lane * 8;
+        if (col < K) {
+          d[col / 8] = code[u];
+          if ((lane & 3) == 0) s[col / kBlock] = (uint8_t)b[u];
+        }
+      }
+      if (c0 + kChunk >= K && pad0 + lane < pitch) s[pad0 + lane] = 0;
+    };
+    if constexpr (SORTED) {
+      for (int j = 0; j < k; ++j) {
+        const int p = __ldg(pair_pos + row * k + j);
+        if (p >= 0 && p < P) store(p);
+      }
+    } else {
+      store(row);
+    }
+  }
+  if constexpr (SORTED) {
+    for (int64_t r = max(0, __ldg(offsets + E)) + warp0; r < P; r += warps) {
+      for (int i = lane; i < K / 8; i += 32) data[r * (K / 8) + i] = 0u;
+      for (int i = lane; i < pitch; i += 32) scale[r * pitch + i] = 0;
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(QTHREADS) dequantize_kernel(const uint32_t* __restrict__ data,
+                                                              const uint8_t* __restrict__ scale, int64_t rows, int K,
+                                                              int pitch, int chunks, T* __restrict__ out) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp0 = (int64_t)blockIdx.x * (QTHREADS / 32) + (threadIdx.x >> 5);
+  const int64_t warps = (int64_t)gridDim.x * (QTHREADS / 32);
+  for (int64_t it = warp0; it < rows * chunks; it += warps) {
+    const int64_t row = it / chunks;
+    const int c0 = (int)(it - row * chunks) * kChunk;
+    uint32_t w[kPasses], b[kPasses];
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      const int col = c0 + u * 256 + lane * 8;
+      w[u] = col < K ? __ldcs(data + row * (K / 8) + col / 8) : 0u;
+      b[u] = col < K ? __ldg(scale + row * pitch + col / kBlock) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < kPasses; ++u) {
+      const int col = c0 + u * 256 + lane * 8;
+      if (col >= K) break;
+      float f[8];
+      unpack8(w[u], f);
+      const float s = scale_value(b[u]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] *= s;
+      T* o = out + row * K + col;
+      if constexpr (sizeof(T) == 4) {
+        reinterpret_cast<float4*>(o)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4*>(o)[1] = make_float4(f[4], f[5], f[6], f[7]);
+      } else {
+        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                  pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+      }
+    }
+  }
+}
+
+bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+unsigned warp_grid(int64_t items) {
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, QTHREADS / 32), 148 * 8));
+}
+
+moe_status check_rows(int64_t rows, int64_t K, int32_t dtype) {
+  if (rows < 0 || K <= 0 || K % kBlock != 0 || K >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31))
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (dtype != MOE_DTYPE_F32 && dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+moe_status status(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+}  // namespace
+}  // namespace stm
+
+using namespace stm;
+
+MOE_API moe_status moe_mx4_quantize(int64_t rows, int64_t K, int32_t dtype, const void* x, void* data, void* scale,
+                                    moe_stream_t stream) {
+  const moe_status st = check_rows(rows, K, dtype);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(data) || !ok_ptr(scale)) return MOE_ERR_INVALID_ARGUMENT;
+  const int chunks = (int)ceil_div(K, kChunk), pitch = (int)scale_pitch(K);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* d = static_cast<uint32_t*>(data);
+  uint8_t* sc = static_cast<uint8_t*>(scale);
+  if (dtype == MOE_DTYPE_F32)
+    quantize_kernel<float, false><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(
+        static_cast<const float*>(x), rows, (int)K, d, sc, pitch, chunks, nullptr, nullptr, 1, 0);
+  else
+    quantize_kernel<__nv_bfloat16, false><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(x), rows, (int)K, d, sc, pitch, chunks, nullptr, nullptr, 1, 0);
+  return status(cudaGetLastError());
+}
+
+MOE_API moe_status moe_mx4_dequantize(int64_t rows, int64_t K, int32_t dtype, const void* data, const void* scale,
+                                      void* out, moe_stream_t stream) {
+  const moe_status st = check_rows(rows, K, dtype);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!ok_ptr(data) || !ok_ptr(scale) || !ok_ptr(out)) return MOE_ERR_INVALID_ARGUMENT;
+  const int chunks = (int)ceil_div(K, kChunk), pitch = (int)scale_pitch(K);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const uint32_t* d = static_cast<const uint32_t*>(data);
+  const uint8_t* sc = static_cast<const uint8_t*>(scale);
+  if (dtype == MOE_DTYPE_F32)
+    dequantize_kernel<float><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(d, sc, rows, (int)K, pitch, chunks,
+                                                                           static_cast<float*>(out));
+  else
+    dequantize_kernel<__nv_bfloat16><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(
+        d, sc, rows, (int)K, pitch, chunks, static_cast<__nv_bfloat16*>(out));
+  return status(cudaGetLastError());
+}
+
+MOE_API moe_status moe_mx4_permute_rows(const moe_problem* p, const void* x, const int32_t* pair_pos,
+                                        const int32_t* offsets, void* data, void* scale, moe_stream_t stream) {
+  size_t bytes = 0;
+  const moe_status st = moe_workspace_size(p, &bytes);  // validates the problem
+  if (st != MOE_OK) return st;
+  if (p->H % kBlock != 0) return MOE_ERR_INVALID_ARGUMENT;
+  if (p->T == 0) return MOE_OK;
+  if (!ok_ptr(x) || !ok_ptr(pair_pos) || !ok_ptr(offsets) || !ok_ptr(data) || !ok_ptr(scale))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const int chunks = (int)ceil_div(p->H, kChunk), pitch = (int)scale_pitch(p->H);
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  uint32_t* d = static_cast<uint32_t*>(data);
+  uint8_t* sc = static_cast<uint8_t*>(scale);
+  if (p->dtype == MOE_DTYPE_F32)
+    quantize_kernel<float, true><<<warp_grid(p->T * chunks), QTHREADS, 0, s>>>(
+        static_cast<const float*>(x), p->T, (int)p->H, d, sc, pitch, chunks, pair_pos, offsets, (int)p->k, (int)p->E);
+  else
+    quantize_kernel<__nv_bfloat16, true><<<warp_grid(p->T * chunks), QTHREADS, 0, s>>>(
+        static_cast<const __nv_bfloat16*>(x), p->T, (int)p->H, d, sc, pitch, chunks, pair_pos, offsets, (int)p->k,
+        (int)p->E);
+  return status(cudaGetLastError());
+}

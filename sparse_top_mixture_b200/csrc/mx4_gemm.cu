@@ -1,0 +1,625 @@
+// Grouped products of microscaled 4-bit rows with 4-bit expert weights, on the
+// block-scaled tensor cores (tcgen05.mma kind::mxf4; the format is in
+// mx4.cuh). Over the segments of the dispatch's offsets, for each row p of
+// segment e:
+//   product   out[p, n] = sum_b 2^(sa[p,b] + sw[e,n,b] - 254) sum_{i<32} a w
+//   gate_up   h[p, n] = silu(product with the gate row n) * (... up row n),
+//             bf16, or rounded to bf16 and then quantised to 4 bits
+//
+// The MMA multiplies 64 values of K at a time by their two scale bytes per row
+// and accumulates in fp32; nothing is dequantised. Large batches are bound by
+// getting operands to the tensor cores (at 4 bits a 128 x 192 x 256 step needs
+// 40 KB for 384 clocks of MMA), small ones by streaming the experts' weights
+// from HBM once.
+//
+// Design (one CTA per SM, persistent, warp-specialised, 256 threads):
+//   warp 0     TMA producer: the tile's rows of A in boxes of 32 x 128 bytes
+//              (256 values of K; only as many boxes as the tile has rows), and
+//              B in units of 64 rows: 64 rows of W, or for gate_up 32 gate
+//              rows and the 32 up rows of the same features (one box of a 4-D
+//              map), so a unit holds both halves of 32 outputs.
+//   warp 1     TMEM allocator and MMA issuer: per step it copies the step's
+//              scales from shared memory to TMEM (tcgen05.cp) and issues up to
+//              four MMAs, M 128, N 64 per unit. Two accumulators.
+//   warps 2, 3 scale producers for A and B: the tensor core wants the four
+//              scale bytes of a row's 128 values as one word, row r at lane
+//              r % 32 and column r / 32. A lane loads 16 scale bytes (512
+//              values) of its rows r, r+32, ... from their plain row-major
+//              places and stores the transposed words, so neither rows nor
+//              weights need a layout of their own and a segment may start at
+//              any row.
+//   warps 4..7 epilogue: TMEM to registers, SwiGLU / rounding / quantisation
+//              of a lane's own row, 16-byte stores of 64-byte pieces through
+//              a swizzled staging buffer; rows past the segment are dropped.
+// A tile is 128 rows by 1..3 units. Every CTA picks the units per tile from the
+// number of row tiles, which only the device knows (choose_units). The ring's
+// stage size follows the units, and its depth the stage size.
+//
+// Waits are bounded as in gemm_tc.cu.
+#include <cuda.h>
+
+#include <mutex>
+
+#include "kernels.h"
+#include "mx4.cuh"
+#include "tc_ptx.cuh"
+#include "tiles.cuh"
+
+#define MOE_API extern "C" __attribute__((visibility("default")))
+
+namespace stm {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 128;
+constexpr int BK = 256;              // values per step: 128 data bytes, one swizzle row
+constexpr int UNIT = 64;             // B rows per unit
+constexpr int MAX_UNITS = 3;
+constexpr int A_BYTES = BM * BK / 2;
+constexpr int A_BOX_BYTES = 32 * BK / 2;
+constexpr int UNIT_BYTES = UNIT * BK / 2;
+constexpr int SF_ATOM_BYTES = 512;   // scale words of 128 rows for 128 values of K
+constexpr int SFA_BYTES = 2 * SF_ATOM_BYTES;
+constexpr int MAX_STAGES = 8;
+constexpr int ACC_COLS = MAX_UNITS * UNIT;       // TMEM columns of one accumulator
+constexpr int SF_COL = 2 * ACC_COLS;             // two sets of scale columns follow
+constexpr int SF_SET_COLS = 2 * 4 + 2 * 8;       // two atoms of A, two of B (up to 256 rows)
+constexpr int TMEM_COLS = 512;
+static_assert(SF_COL + 2 * SF_SET_COLS <= TMEM_COLS, "accumulators and scales fit TMEM");
+constexpr int GTHREADS = 256;
+constexpr int STAGING_BYTES = 32 * 64;           // per epilogue warp
+
+__host__ __device__ constexpr int sfb_blocks(int units) { return (units * UNIT + 127) / 128; }
+__host__ __device__ constexpr int stage_bytes(int units) {
+  return A_BYTES + units * UNIT_BYTES + SFA_BYTES + 2 * sfb_blocks(units) * SF_ATOM_BYTES;
+}
+constexpr int RING_BYTES = 5 * stage_bytes(3);
+__host__ __device__ constexpr int ring_stages(int units) {
+  return RING_BYTES / stage_bytes(units) < MAX_STAGES ? RING_BYTES / stage_bytes(units) : MAX_STAGES;
+}
+
+enum { OUT_BF16 = 0, OUT_F32 = 1, SWIGLU_BF16 = 2, SWIGLU_MX4 = 3 };
+constexpr bool is_swiglu(int mode) { return mode >= SWIGLU_BF16; }
+
+struct Args {
+  const int32_t* offsets;
+  int32_t E;
+  int64_t rows_total;
+  int32_t N;         // output columns (gate_up: I)
+  int32_t n_units;   // 64-row units of B per expert
+  int32_t k_steps;
+  int32_t K;
+  const uint8_t* a_scale;
+  const uint8_t* b_scale;
+  int32_t pitch;     // scale bytes per row of K values
+  int64_t b_rows;    // B rows per expert
+  void* out;         // bf16 / fp32 [rows, N], or data bytes [rows, N/2]
+  uint8_t* out_scale;
+  int32_t out_pitch;
+  int32_t* err;
+};
+
+struct __align__(8) Ctl {
+  uint64_t full[MAX_STAGES];
+  uint64_t empty[MAX_STAGES];
+  uint64_t tfull[2];
+  uint64_t tempty[2];
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int units;
+  int off[kMaxExperts + 1];
+  int pre[kMaxExperts + 1];
+};
+
+constexpr size_t kSmemBytes = 1024 + (size_t)RING_BYTES + 4 * STAGING_BYTES + sizeof(Ctl);
+static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
+
+// Instruction descriptor, kind::mxf4: A and B e2m1 (bits 7-9, 10-12 = 1), K
+// major, N>>3 in bits 17-22, scales ue8m0 (bit 23), M>>4 in 24-28; which half
+// of the scale words (0, or 2 for the second 64 values) in bits 4-5 for B and
+// 29-30 for A.
+__device__ __forceinline__ uint32_t make_idesc_mxf4(int N, uint32_t half) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 4) << 24) |
+         (half << 4) | (half << 29);
+}
+
+// Shared-memory descriptor of one scale atom for tcgen05.cp: 32 rows of 16
+// bytes, no swizzle, 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+}
+
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                          uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// Units per tile: the fewest rounds of tiles over the grid, each weighed by the
+// operand bytes of its tiles (8 KB a unit and step, 4 KB for each 32 rows of A
+// that the average tile has). Few row tiles take narrow tiles, so that every
+// SM streams weights; many take wide ones, which re-read A least.
+__device__ __forceinline__ int choose_units(int row_tiles, int rows, int n_units, int grid) {
+  const int boxes = row_tiles > 0 ? min(4, (rows / row_tiles + 31) / 32) : 1;
+  int best = MAX_UNITS;
+  long long least = -1;
+  for (int u = MAX_UNITS; u >= 1; --u) {
+    const long long tiles = (long long)row_tiles * ((n_units + u - 1) / u);
+    const long long cost = (tiles + grid - 1) / grid * (2 * u + max(1, boxes));
+    if (least < 0 || cost < least) {
+      least = cost;
+      best = u;
+    }
+  }
+  return best;
+}
+
+struct Tile {
+  int e, row0, row_end, unit0, units;
+};
+
+__device__ __forceinline__ Tile decode(const Ctl* ctl, const Args& a, int units, int n_tiles, int tile) {
+  Tile t;
+  const int mt = tile / n_tiles;
+  t.unit0 = (tile - mt * n_tiles) * units;
+  t.units = min(units, a.n_units - t.unit0);
+  t.e = find_segment(ctl->pre, a.E, mt);
+  t.row0 = ctl->off[t.e] + (mt - ctl->pre[t.e]) * BM;
+  t.row_end = ctl->off[t.e + 1];
+  return t;
+}
+
+// One lane's four 16-byte pieces of a 64-byte row piece into the warp's staging
+// buffer (row = lane), then out again as 16-byte stores of whole row pieces,
+// four lanes to a row. A piece's place in its row is rotated by the row, so
+// that neither side has bank conflicts.
+__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint8_t* stage, uint8_t* out, int64_t row_bytes,
+                                             int nrows, int bytes, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) = v[c];
+  __syncwarp();
+  const int c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + 16 * (c ^ ((r >> 1) & 3)));
+    if (r < nrows && c * 16 < bytes) *reinterpret_cast<uint4*>(out + r * row_bytes + c * 16) = w;
+  }
+}
+
+template <int MODE>
+__global__ void __launch_bounds__(GTHREADS, 1)
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args args) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* staging = base + RING_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(staging + 4 * STAGING_BYTES);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < MAX_STAGES; ++s) {
+      mbar_init(&ctl->full[s], 3);  // TMA, and the two scale warps
+      mbar_init(&ctl->empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&ctl->tfull[a], 1);
+      mbar_init(&ctl->tempty[a], 128);
+    }
+    mbar_init(&ctl->drain, 1);
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 2) {
+    warp_build_tile_table(args.offsets, args.E, 0, BM, ctl->off, ctl->pre, args.rows_total, args.err);
+    __syncwarp();
+    if (lane == 0) {
+      const int row_tiles = ctl->pre[args.E];
+      ctl->units = choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units,
+                                (int)gridDim.x);
+    }
+  }
+  if (warp == 1) tmem_alloc(&ctl->tmem_base, TMEM_COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = ctl->tmem_base;
+  const int units = ctl->units;
+  const int n_tiles = (args.n_units + units - 1) / units;
+  const int total = ctl->pre[args.E] * n_tiles;
+  const int stages = ring_stages(units), sbytes = stage_bytes(units);
+  const int sfa_off = A_BYTES + units * UNIT_BYTES, sfb_off = sfa_off + SFA_BYTES;
+  const int blocks = sfb_blocks(units);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      int stage = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = decode(ctl, args, units, n_tiles, tile);
+        const int boxes = min(4, (t.row_end - t.row0 + 31) / 32);
+        for (int kt = 0; kt < args.k_steps; ++kt) {
+          if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
+            ok = false;
+            break;
+          }
+          uint8_t* sa = base + stage * sbytes;
+          mbar_arrive_expect_tx(&ctl->full[stage], (uint32_t)(boxes * A_BOX_BYTES + t.units * UNIT_BYTES));
+          const int kb = kt * (BK / 2);
+          for (int i = 0; i < boxes; ++i)
+            tma_load_2d(sa + i * A_BOX_BYTES, &tmA, &ctl->full[stage], kb, t.row0 + 32 * i);
+          for (int j = 0; j < t.units; ++j)
+            tma_load_4d(sa + A_BYTES + j * UNIT_BYTES, &tmB, &ctl->full[stage], kb,
+                        (t.unit0 + j) * (is_swiglu(MODE) ? UNIT / 2 : UNIT), 0, t.e);
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      // Every copy has landed before the CTA may exit. The full barrier of a
+      // stage also counts the scale warps' arrivals, which make every stage
+      // they can reach unless the kernel gives up.
+      for (int s = 0; s < stages; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // ---------------- MMA issuer ----------------
+      int stage = 0, acc = 0, set = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = decode(ctl, args, units, n_tiles, tile);
+        if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+        const uint32_t idesc0 = make_idesc_mxf4(t.units * UNIT, 0), idesc2 = make_idesc_mxf4(t.units * UNIT, 2);
+        for (int kt = 0; kt < args.k_steps; ++kt) {
+          if (!mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(base + stage * sbytes);
+          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS, sfb = sfa + 8;
+#pragma unroll
+          for (int atom = 0; atom < 2; ++atom) {
+            copy_scales(sfa + 4 * atom, sf_desc(sa + sfa_off + atom * SF_ATOM_BYTES));
+            for (int b = 0; b < blocks; ++b)
+              copy_scales(sfb + 8 * atom + 4 * b, sf_desc(sa + sfb_off + (atom * blocks + b) * SF_ATOM_BYTES));
+          }
+          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
+          const int left = (args.K - kt * BK + 63) / 64;  // 64-value pieces of K left
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (kk < left)
+              umma_mxf4(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, (kk & 1) ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
+                        sfb + 8 * (kk >> 1), (kt > 0 || kk > 0) ? 1u : 0u);
+          umma_commit(&ctl->empty[stage]);
+          set ^= 1;
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+        if (!ok) break;
+        umma_commit(&ctl->tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
+      }
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
+    }
+  } else if (warp < 4) {
+    // ---------------- scale producers (warp 2: A, warp 3: B) ----------------
+    constexpr int kMaxRows = MAX_UNITS * UNIT / 32;  // row slots of a lane, A has 4
+    const bool is_b = warp == 3;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(ctl, args, units, n_tiles, tile);
+      const uint4* src[kMaxRows];  // this lane's rows' scales, nullptr for a row that the tile lacks
+      if (is_b) {
+        const uint8_t* w = args.b_scale + (int64_t)t.e * args.b_rows * args.pitch;
+#pragma unroll
+        for (int c = 0; c < kMaxRows; ++c) {
+          // gate_up: the unit's 32 gate rows, then its 32 up rows
+          const int n = is_swiglu(MODE) ? (t.unit0 + (c >> 1)) * 32 + lane : t.unit0 * UNIT + 32 * c + lane;
+          const int64_t row = is_swiglu(MODE) ? (int64_t)(c & 1) * args.N + n : n;
+          src[c] = c < 2 * t.units && n < args.N ? reinterpret_cast<const uint4*>(w + row * args.pitch) : nullptr;
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < kMaxRows; ++c) {
+          const int row = t.row0 + 32 * c + lane;
+          src[c] = c < 4 && row < t.row_end
+                       ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch)
+                       : nullptr;
+        }
+      }
+      uint4 next[kMaxRows];
+#pragma unroll
+      for (int c = 0; c < kMaxRows; ++c) next[c] = src[c] ? __ldg(src[c]) : make_uint4(0, 0, 0, 0);
+      for (int kt = 0; ok && kt < args.k_steps; kt += 2) {
+        uint4 v[kMaxRows];
+#pragma unroll
+        for (int c = 0; c < kMaxRows; ++c) v[c] = next[c];
+        if (kt + 2 < args.k_steps) {
+#pragma unroll
+          for (int c = 0; c < kMaxRows; ++c)
+            if (src[c]) next[c] = __ldg(src[c] + (kt >> 1) + 1);
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (kt + h >= args.k_steps) break;
+          const bool got = mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 5);
+          if (!__all_sync(0xffffffffu, got)) {
+            ok = false;
+            break;
+          }
+          uint8_t* dst = base + stage * sbytes + (is_b ? sfb_off : sfa_off) + lane * 16;
+          const int nb = is_b ? blocks : 1;
+#pragma unroll
+          for (int atom = 0; atom < 2; ++atom) {
+            // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
+            const int valid = args.K / mx4::kBlock - (kt + h) * 8 - atom * 4;
+            const uint32_t mask = valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+            auto word = [&](int c) {
+              if (c >= kMaxRows) return 0u;
+              const uint4& q = v[c];
+              return mask & (h == 0 ? (atom == 0 ? q.x : q.y) : (atom == 0 ? q.z : q.w));
+            };
+            *reinterpret_cast<uint4*>(dst + atom * nb * SF_ATOM_BYTES) = make_uint4(word(0), word(1), word(2), word(3));
+            if (nb == 2)
+              *reinterpret_cast<uint4*>(dst + (atom * nb + 1) * SF_ATOM_BYTES) = make_uint4(word(4), word(5), 0u, 0u);
+          }
+          fence_to_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->full[stage]);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+    }
+  } else {
+    // ---------------- epilogue (warps 4..7) ----------------
+    const int quarter = warp & 3;  // TMEM lanes this warp may access
+    uint8_t* stg = staging + quarter * STAGING_BYTES;
+    int acc = 0;
+    uint32_t acc_phase = 0;
+    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+      const Tile t = decode(ctl, args, units, n_tiles, tile);
+      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, &ctl->abort, args.err, 4))) break;
+      tc_fence_after();
+      const int row_w0 = t.row0 + quarter * 32;
+      const int nrows = min(32, t.row_end - row_w0);
+      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+      if (nrows > 0) {
+#pragma unroll 1
+        for (int j = 0; j < t.units; ++j) {
+          uint32_t g[32], u[32];
+          tmem_ld32(tbase + j * UNIT, g);
+          tmem_ld32(tbase + j * UNIT + 32, u);
+          tmem_ld_wait_regs(g);
+          tmem_ld_wait_regs(u);
+          if constexpr (is_swiglu(MODE)) {
+            const int n0 = (t.unit0 + j) * 32;  // N is a multiple of 32: the block lies inside
+            uint32_t h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              h[i] = pack_bf16x2(silu_f32(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
+                                 silu_f32(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+            if constexpr (MODE == SWIGLU_BF16) {
+              uint4 v[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) v[c] = make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+              store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + n0) * 2,
+                           (int64_t)args.N * 2, nrows, 64, lane);
+            } else {
+              // the lane's own row: 32 values, one scale
+              uint32_t m = 0;
+#pragma unroll
+              for (int i = 0; i < 16; ++i) m = max(m, max((h[i] << 16) & 0x7fffffffu, h[i] & 0x7fff0000u));
+              const uint32_t b = mx4::scale_byte(m);
+              const float inv = mx4::inverse_scale(b);
+              uint32_t code[4];
+#pragma unroll
+              for (int c = 0; c < 4; ++c) {
+                float f[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  f[2 * i] = __uint_as_float(h[4 * c + i] << 16) * inv;
+                  f[2 * i + 1] = __uint_as_float(h[4 * c + i] & 0xffff0000u) * inv;
+                }
+                code[c] = b == mx4::kScaleNaN ? 0u : mx4::pack8(f);
+              }
+              if (lane < nrows) {
+                const int64_t row = row_w0 + lane;
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0) / 2) =
+                    make_uint4(code[0], code[1], code[2], code[3]);
+                uint8_t* s = args.out_scale + row * args.out_pitch;
+                s[n0 / 32] = (uint8_t)b;
+                if (n0 + 32 == args.N)  // the row's last block also writes the padding
+                  for (int i = args.N / 32; i < args.out_pitch; ++i) s[i] = 0;
+              }
+            }
+          } else {
+            const int n0 = (t.unit0 + j) * UNIT;
+            if constexpr (MODE == OUT_BF16) {
+#pragma unroll
+              for (int half = 0; half < 2; ++half) {
+                const int nh = n0 + 32 * half;
+                if (nh >= args.N) break;
+                uint4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  uint32_t p[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    p[i] = half == 0 ? pack_bf16x2(__uint_as_float(g[8 * c + 2 * i]), __uint_as_float(g[8 * c + 2 * i + 1]))
+                                     : pack_bf16x2(__uint_as_float(u[8 * c + 2 * i]), __uint_as_float(u[8 * c + 2 * i + 1]));
+                  v[c] = make_uint4(p[0], p[1], p[2], p[3]);
+                }
+                store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + nh) * 2,
+                             (int64_t)args.N * 2, nrows, 2 * (args.N - nh), lane);
+              }
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int nh = n0 + 16 * q;
+                if (nh >= args.N) break;
+                uint4 v[4];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  const uint32_t* d = q < 2 ? g : u;
+                  const int o = 16 * (q & 1) + 4 * c;
+                  v[c] = make_uint4(d[o], d[o + 1], d[o + 2], d[o + 3]);
+                }
+                store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + nh) * 4,
+                             (int64_t)args.N * 4, nrows, 4 * (args.N - nh), lane);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&ctl->tempty[acc]);
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
+template <int MODE>
+cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_data, const void* a_scale,
+                   const int32_t* offsets, const void* w_data, const void* w_scale, void* out, void* out_scale,
+                   int32_t* err, cudaStream_t s) {
+  static std::once_flag once[kSmemAttrDevices];  // one set per kernel instance
+  static cudaError_t attr[kSmemAttrDevices];
+  const void* kernel = reinterpret_cast<const void*>(mx4_gemm_kernel<MODE>);
+  const cudaError_t e = set_max_dynamic_smem_once(kernel, (int)kSmemBytes, once, attr);
+  if (e != cudaSuccess) return e;
+  if (!get_encode()) return cudaErrorNotSupported;
+  CUtensorMap tmA, tmB;
+  {
+    const uint64_t dims[2] = {(uint64_t)K / 2, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)K / 2};
+    const uint32_t box[2] = {BK / 2, 32};
+    if (!make_tensor_map_u8(&tmA, a_data, 2, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  {
+    // W [E][halves][N][K/2]: gate_up's two halves, or one
+    const uint64_t halves = is_swiglu(MODE) ? 2 : 1;
+    const uint64_t dims[4] = {(uint64_t)K / 2, (uint64_t)N, halves, (uint64_t)E};
+    const uint64_t strides[3] = {(uint64_t)K / 2, (uint64_t)N * K / 2, halves * (uint64_t)N * K / 2};
+    const uint32_t box[4] = {BK / 2, (uint32_t)(UNIT / halves), (uint32_t)halves, 1};
+    if (!make_tensor_map_u8(&tmB, w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
+  }
+  Args a{};
+  a.offsets = offsets;
+  a.E = (int32_t)E;
+  a.rows_total = rows;
+  a.N = (int32_t)N;
+  a.n_units = (int32_t)ceil_div(N, is_swiglu(MODE) ? UNIT / 2 : UNIT);
+  a.k_steps = (int32_t)ceil_div(K, BK);
+  a.K = (int32_t)K;
+  a.a_scale = static_cast<const uint8_t*>(a_scale);
+  a.b_scale = static_cast<const uint8_t*>(w_scale);
+  a.pitch = (int32_t)mx4::scale_pitch(K);
+  a.b_rows = N * (is_swiglu(MODE) ? 2 : 1);
+  a.out = out;
+  a.out_scale = static_cast<uint8_t*>(out_scale);
+  a.out_pitch = (int32_t)mx4::scale_pitch(N);
+  a.err = err;
+  const int64_t most = (rows / BM + std::min<int64_t>(rows, E)) * a.n_units;  // tiles of one unit
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms(), most));
+  mx4_gemm_kernel<MODE><<<grid, GTHREADS, kSmemBytes, s>>>(tmA, tmB, a);
+  return cudaGetLastError();
+}
+
+bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// rows, E, N, K of a product; tiles are counted in 32 bits.
+moe_status check_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, int64_t n_multiple) {
+  const int64_t lim = int64_t(1) << 31;
+  if (rows < 0 || rows >= lim || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= lim)
+    return MOE_ERR_INVALID_ARGUMENT;
+  if (K % mx4::kBlock != 0 || N % n_multiple != 0) return MOE_ERR_INVALID_ARGUMENT;
+  if ((rows / BM + E) * ceil_div(N, 32) >= lim) return MOE_ERR_INVALID_ARGUMENT;
+  return MOE_OK;
+}
+
+bool ok_ws(const void* ws) { return (reinterpret_cast<uintptr_t>(ws) & 15u) == 0; }
+
+}  // namespace
+}  // namespace stm
+
+using namespace stm;
+
+MOE_API moe_status moe_mx4_grouped_matmul(int64_t rows, int64_t E, int64_t N, int64_t K, int32_t out_dtype,
+                                          const void* a_data, const void* a_scale, const int32_t* offsets,
+                                          const void* w_data, const void* w_scale, void* out, void* ws,
+                                          moe_stream_t stream) {
+  const moe_status st = check_sizes(rows, E, N, K, 8);
+  if (st != MOE_OK) return st;
+  if (out_dtype != MOE_DTYPE_F32 && out_dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARGUMENT;
+  if (rows == 0) return MOE_OK;
+  if (!ok_ptr(a_data) || !ok_ptr(a_scale) || !ok_ptr(offsets) || !ok_ptr(w_data) || !ok_ptr(w_scale) || !ok_ptr(out) ||
+      !ok_ws(ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* err = static_cast<int32_t*>(ws);
+  const cudaError_t e =
+      out_dtype == MOE_DTYPE_F32
+          ? launch<OUT_F32>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s)
+          : launch<OUT_BF16>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+MOE_API moe_status moe_mx4_grouped_gate_up(int64_t rows, int64_t E, int64_t I, int64_t H, const void* a_data,
+                                           const void* a_scale, const int32_t* offsets, const void* w_data,
+                                           const void* w_scale, void* h, void* h_scale, void* ws,
+                                           moe_stream_t stream) {
+  const moe_status st = check_sizes(rows, E, I, H, 32);
+  if (st != MOE_OK) return st;
+  if (rows == 0) return MOE_OK;
+  if (!ok_ptr(a_data) || !ok_ptr(a_scale) || !ok_ptr(offsets) || !ok_ptr(w_data) || !ok_ptr(w_scale) || !ok_ptr(h) ||
+      !ok_ws(h_scale) || !ok_ws(ws))
+    return MOE_ERR_INVALID_ARGUMENT;
+  const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* err = static_cast<int32_t*>(ws);
+  const cudaError_t e =
+      h_scale == nullptr
+          ? launch<SWIGLU_BF16>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, nullptr, err, s)
+          : launch<SWIGLU_MX4>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, h_scale, err, s);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}

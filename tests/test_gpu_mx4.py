@@ -1,0 +1,453 @@
+"""Microscaled 4-bit quantisation and the grouped products against plain
+implementations in 64 bits.
+
+Tolerances, from the arithmetic alone: quantisation and dequantisation have
+one result. A product's terms (4-bit times 4-bit times two powers of two) are
+exact in fp32; accumulating them in fp32 in blocks of at least 32 loses at most
+2^-22 of the terms' summed magnitudes per block (half a step of rounding, or a
+whole one if it truncates, for the block's own sum and for the running one),
+so K/32 + 2 such steps bound it. Rounding to bf16 adds 2^-8 of the value. SwiGLU:
+|d silu/dg| <= 1.1, and exp, the division and the products in fp32 lose at most
+2^-20 of the result."""
+
+import ctypes
+
+import pytest
+import torch
+
+import sparse_top_mixture_b200 as stm
+import workloads
+from workloads import CONFIGS, reduced
+
+pytestmark = pytest.mark.gpu
+
+GRID = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=torch.float64)
+
+
+def ref_quantize(x):
+    """(values, scale bytes) of x [rows, K] by the definition, in 64 bits on the CPU."""
+    b = x.double().cpu().reshape(-1, 32)
+    m = b.abs().amax(1)
+    bad = ~torch.isfinite(b).all(1)
+    _, e = torch.frexp(torch.where(bad, 1.0, m))
+    byte = torch.where(m > 0, (e - 1 - 2 + 127).clamp(min=0), 0)
+    unit = torch.ldexp(torch.ones_like(m), byte - 127)
+    a = torch.where(bad[:, None], 0.0, b).abs() / unit[:, None]
+    d = (a[:, :, None] - GRID).abs()
+    near = d == d.amin(2, keepdim=True)
+    even = near & (torch.arange(8) % 2 == 0)
+    pick = torch.where(even.any(2), even.int().argmax(2), near.int().argmax(2))
+    v = torch.where(b < 0, -1.0, 1.0) * GRID[pick] * unit[:, None]
+    v[bad], byte[bad] = float("nan"), 255
+    rows, K = x.shape
+    return v.reshape(rows, K), byte.reshape(rows, K // 32).to(torch.uint8)
+
+
+def ref_values(q):
+    """The values of an Mx4 in 64 bits, on its device."""
+    data, K = q.data.long(), q.K
+    code = torch.stack((data & 15, data >> 4), -1).reshape(*data.shape[:-1], K)
+    grid = torch.cat((GRID, -GRID)).to(data.device)
+    s = q.scale[..., : K // 32].long()
+    # 2^(s - 127) by its fp64 exponent field (a device's pow is not exact)
+    unit = torch.where(s == 255, torch.nan, ((s - 127 + 1023) << 52).view(torch.float64))
+    return grid[code] * unit.repeat_interleave(32, -1)
+
+
+def same(a, b):
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+def _rand(shape, dtype=torch.bfloat16, seed=1, std=1.0):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype).cuda()
+
+
+# ---- quantisation -----------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,K", [(1, 32), (3, 64), (5, 96), (2, 512), (7, 544), (300, 1024), (4, 1056), (33, 7168),
+                                    (20000, 32), (1, 32 * 700)])
+def test_quantize(rows, K, dtype):
+    x = _rand((rows, K), dtype, rows + K)
+    x *= torch.exp2(torch.randint(-60, 60, (rows, 1), generator=torch.Generator().manual_seed(3)).float()).cuda().to(dtype)
+    q = stm.mx4_quantize(x)
+    v, byte = ref_quantize(x)
+    assert q.K == K and q.shape == (rows, K)
+    assert torch.equal(q.scale[:, : K // 32].cpu(), byte)
+    assert int(q.scale[:, K // 32:].sum()) == 0
+    assert same(ref_values(q).cpu(), v)
+    for out in (torch.float32, torch.bfloat16):
+        assert same(stm.mx4_dequantize(q, out).double().cpu(), v.to(out).double())
+
+
+def test_quantize_the_hard_blocks():
+    """Zeros of both signs, infinities, NaN, the smallest and the largest
+    magnitudes, exact powers of two, and every tie and its neighbours."""
+    half = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 7.0])
+    ties = torch.cat([half, -half, torch.nextafter(half, torch.tensor(9.0)), -torch.nextafter(half, torch.tensor(0.0))])
+    blocks = []
+    for scale in (2.0 ** -127, 2.0 ** -120, 1.0, 2.0 ** 20, 2.0 ** 124):
+        blocks.append(torch.cat([ties[:16], torch.full((16,), 4.0)]) * scale)
+        blocks.append(torch.cat([ties[16:], torch.full((16,), 7.9375)]) * scale)
+    blocks += [torch.zeros(32), -torch.zeros(32), torch.full((32,), 2.0 ** -133), torch.full((32,), 2.0 ** -149),
+               torch.full((32,), torch.finfo(torch.float32).max)]
+    for special in (float("inf"), -float("inf"), float("nan")):
+        b = torch.ones(32)
+        b[13] = special
+        blocks.append(b)
+    blocks += [torch.full((32,), 2.0 ** i) for i in range(-130, 128)]
+    x32 = torch.stack(blocks)
+    for x in (x32, x32.to(torch.bfloat16)):
+        q = stm.mx4_quantize(x.reshape(-1, 32).cuda())
+        v, byte = ref_quantize(x)
+        assert torch.equal(q.scale[:, :1].cpu(), byte)
+        assert same(ref_values(q).cpu(), v)
+
+
+def test_dequantize_every_code_and_scale():
+    data = torch.arange(256, dtype=torch.uint8).repeat(256, 1).cuda()          # K = 512
+    scale = torch.arange(256, dtype=torch.uint8)[:, None].repeat(1, 16).cuda()
+    q = stm.Mx4(data, scale)
+    v = ref_values(q).cpu()
+    for out in (torch.float32, torch.bfloat16):
+        assert same(q.dequantize(out).double().cpu(), v.to(out).double())
+
+
+def test_quantize_shapes():
+    x = _rand((3, 5, 64))
+    q = stm.mx4_quantize(x)
+    assert q.shape == (3, 5, 64) and q.data.shape == (3, 5, 32) and q.scale.shape == (3, 5, 16)
+    assert torch.equal(q.dequantize(), stm.mx4_quantize(x.reshape(15, 64)).dequantize().reshape(3, 5, 64))
+    one = stm.mx4_quantize(x[0, 0])
+    assert one.shape == (64,) and torch.equal(one.data, q.data[0, 0])
+    none = stm.mx4_quantize(x[:0])
+    assert none.shape == (0, 5, 64) and none.dequantize().shape == (0, 5, 64)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T,H,E,k,empty", [(1, 32, 1, 1, 0.0), (1, 7168, 256, 8, 0.0), (37, 544, 6, 3, 0.4),
+                                           (300, 2080, 64, 9, 0.2)])
+def test_quantize_into_sorted_order(T, H, E, k, empty, dtype):
+    p = stm.Problem(T=T, H=H, E=E, k=k, I=32, dtype=dtype)
+    g = torch.Generator().manual_seed(T)
+    sel = torch.rand(T, E, generator=g).topk(k, 1).indices
+    sel[torch.rand(T, k, generator=g) < empty] = -1
+    plan = stm.dispatch_slots(p, sel.cuda())
+    x = _rand((T, H), p.torch_dtype, 4)
+    got, ref = stm.mx4_permute_rows(p, x, plan), stm.mx4_quantize(stm.permute_rows(p, x, plan))
+    assert torch.equal(got.data, ref.data) and torch.equal(got.scale, ref.scale)
+
+
+# ---- products ---------------------------------------------------------------
+
+def _offsets(rows, E, seed, kind="spread"):
+    """Segment table [E+1] over `rows` rows; "short" leaves rows on both ends outside."""
+    g = torch.Generator().manual_seed(seed)
+    if kind == "one":
+        off = torch.zeros(E + 1, dtype=torch.int32)
+        off[E // 2 + 1:] = rows
+        return off
+    cut = torch.randint(0, rows + 1, (E + 1,), generator=g).sort().values.int()
+    if kind != "short":
+        cut[0], cut[E] = 0, rows
+    return cut
+
+
+def _operands(rows, E, N, K, seed):
+    a, w = stm.mx4_quantize(_rand((rows, K), seed=seed)), stm.mx4_quantize(_rand((E, N, K), seed=seed + 1, std=K ** -0.5))
+    return a, w
+
+
+def _product(a, w, off):
+    """(product, summed magnitudes) in 64 bits, rows outside the segments NaN."""
+    rows, N = a.data.shape[0], w.data.shape[1]
+    y = torch.full((rows, N), float("nan"), dtype=torch.float64, device="cuda")
+    mag = torch.zeros_like(y)
+    av = ref_values(a)
+    for e, (lo, hi) in enumerate(zip(off[:-1].tolist(), off[1:].tolist())):
+        if hi > lo:
+            we = ref_values(stm.Mx4(w.data[e], w.scale[e]))
+            y[lo:hi], mag[lo:hi] = av[lo:hi] @ we.T, av[lo:hi].abs() @ we.abs().T
+    return y, mag
+
+
+def _steps(K):
+    return (K / 32 + 2) * 2.0 ** -22
+
+
+# rows, E, N, K, kind: single values of everything; odd N and K tails (32 mod 64, 64 mod 256, beyond one scale
+# vector); segments that start anywhere; one to three units per tile, one to many tiles per CTA; many empty experts
+PRODUCTS = [(1, 1, 8, 32, "one"), (3, 4, 40, 64, "spread"), (31, 2, 72, 96, "spread"), (130, 2, 200, 320, "spread"),
+            (129, 1, 64, 256, "one"), (257, 8, 264, 544, "spread"), (128, 256, 64, 1056, "spread"),
+            (500, 5, 1096, 736, "short"), (1500, 3, 1096, 1056, "spread"), (3000, 3, 1096, 512, "spread"),
+            (20000, 7, 648, 288, "spread"), (64, 16, 7168, 2048, "spread"), (40, 3, 512, 7168, "short"),
+            (2048, 4, 2048, 768, "spread"), (90, 9, 96, 160, "one")]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,E,N,K,kind", PRODUCTS)
+def test_grouped_matmul(rows, E, N, K, kind, dtype):
+    a, w = _operands(rows, E, N, K, seed=rows + K)
+    off = _offsets(rows, E, rows + N, kind)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = stm.mx4_grouped_matmul(a, w, off.cuda(), dtype, ws=ws)
+    assert stm.read_device_error(ws) == 0
+    ref, mag = _product(a, w, off)
+    used = slice(int(off[0]), int(off[E]))
+    bound = _steps(K) * mag + (2.0 ** -8 * ref.abs() if dtype == torch.bfloat16 else 0)
+    assert bool(((got.double() - ref).abs() <= bound)[used].all())
+
+
+@pytest.mark.parametrize("rows,E,I,H,kind", [(1, 1, 32, 32, "one"), (3, 4, 64, 64, "spread"),
+                                             (130, 2, 96, 320, "spread"), (257, 8, 160, 544, "spread"),
+                                             (8, 128, 768, 2048, "spread"), (500, 5, 544, 736, "short"),
+                                             (3000, 3, 544, 512, "spread"), (20000, 7, 352, 288, "spread"),
+                                             (2048, 4, 1408, 768, "spread")])
+def test_grouped_gate_up(rows, E, I, H, kind):
+    a, w = _operands(rows, E, 2 * I, H, seed=rows + H)
+    off = _offsets(rows, E, rows + I, kind)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = stm.mx4_grouped_gate_up(a, w, off.cuda(), ws=ws)
+    y, mag = _product(a, w, off)
+    g, u, dg, du = y[:, :I], y[:, I:], _steps(H) * mag[:, :I], _steps(H) * mag[:, I:]
+    silu = g * torch.sigmoid(g)
+    ref = silu * u
+    used = slice(int(off[0]), int(off[E]))
+    bound = 1.1 * dg * (u.abs() + du) + silu.abs() * du + (2.0 ** -8 + 2.0 ** -20) * (ref.abs() + 1.1 * dg * u.abs() + silu.abs() * du)
+    assert bool(((got.double() - ref).abs() <= bound)[used].all())
+    q = stm.mx4_grouped_gate_up(a, w, off.cuda(), quantize=True, ws=ws)
+    assert stm.read_device_error(ws) == 0
+    want = stm.mx4_quantize(got[used].contiguous())
+    assert torch.equal(q.data[used], want.data) and torch.equal(q.scale[used], want.scale)
+
+
+def test_products_are_the_same_every_time():
+    a, w = _operands(3000, 6, 704, 1056, 5)
+    off = _offsets(3000, 6, 5).cuda()
+    first = stm.mx4_grouped_matmul(a, w, off, torch.float32)
+    for _ in range(5):
+        assert torch.equal(stm.mx4_grouped_matmul(a, w, off, torch.float32), first)
+
+
+def test_rows_outside_the_segments_are_left_alone():
+    rows, E, N, K = 300, 4, 200, 320
+    a, w = _operands(rows, E, N, K, 3)
+    off = torch.tensor([37, 37, 180, 181, 250], dtype=torch.int32, device="cuda")
+    for dt, name in ((torch.float32, 0), (torch.bfloat16, 1)):
+        buf = torch.full((rows + 2, N), 7.0, dtype=dt, device="cuda")
+        st = stm.lib().moe_mx4_grouped_matmul(rows, E, N, K, name, a.data.data_ptr(), a.scale.data_ptr(),
+                                              off.data_ptr(), w.data.data_ptr(), w.scale.data_ptr(), buf[1:].data_ptr(),
+                                              None, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        torch.cuda.synchronize()
+        out = buf[1:-1]
+        assert bool((buf[0] == 7).all() and (buf[-1] == 7).all() and (out[:37] == 7).all() and (out[250:] == 7).all())
+        assert torch.equal(out[37:250], stm.mx4_grouped_matmul(a, w, off, dt)[37:250])
+    w2 = stm.mx4_quantize(_rand((E, 192, K), seed=9))
+    data = torch.full((rows, 48), 9, dtype=torch.uint8, device="cuda")
+    scale = torch.full((rows, 16), 9, dtype=torch.uint8, device="cuda")
+    st = stm.lib().moe_mx4_grouped_gate_up(rows, E, 96, K, a.data.data_ptr(), a.scale.data_ptr(), off.data_ptr(),
+                                           w2.data.data_ptr(), w2.scale.data_ptr(), data.data_ptr(), scale.data_ptr(),
+                                           None, torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    for t in (data, scale):
+        assert bool((t[:37] == 9).all() and (t[250:] == 9).all())
+    assert int(scale[37:250, 3:].sum()) == 0
+
+
+def test_nan_scales_stay_in_their_row_and_column():
+    rows, E, N, K = 200, 2, 136, 576
+    x, wt = _rand((rows, K)), _rand((E, N, K), seed=2)
+    x[70, 500], wt[1, 100, 33] = float("nan"), float("inf")
+    a, w = stm.mx4_quantize(x), stm.mx4_quantize(wt)
+    off = torch.tensor([0, 90, 200], dtype=torch.int32, device="cuda")
+    y = stm.mx4_grouped_matmul(a, w, off, torch.float32)
+    want = torch.zeros(rows, N, dtype=torch.bool, device="cuda")
+    want[70], want[90:, 100] = True, True
+    assert torch.equal(y.isnan(), want)
+
+
+def test_padding_of_the_scales_is_never_used():
+    for rows, N, K in ((40, 72, 96), (130, 200, 544), (9, 64, 32)):
+        a, w = _operands(rows, 2, N, K, 8)
+        off = torch.tensor([0, rows // 2, rows], dtype=torch.int32, device="cuda")
+        want = stm.mx4_grouped_matmul(a, w, off, torch.float32)
+        for q in (a, w):
+            q.scale[..., K // 32:] = 255
+        assert torch.equal(stm.mx4_grouped_matmul(a, w, off, torch.float32), want)
+        assert bool(a.dequantize().isfinite().all())
+
+
+def test_a_malformed_table_is_reported_and_computes_nothing():
+    a, w = _operands(100, 3, 64, 64, 1)
+    for off in ([0, 50, 40, 100], [0, 10, 20, 101], [-1, 10, 20, 100]):
+        ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+        off = torch.tensor(off, dtype=torch.int32, device="cuda")
+        stm.mx4_grouped_matmul(a, w, off, ws=ws)
+        assert stm.read_device_error(ws) == stm.DEVERR_BAD_EXPERT_ID
+        stm.mx4_grouped_gate_up(a, w, off, ws=ws)
+        assert stm.read_device_error(ws) == stm.DEVERR_BAD_EXPERT_ID
+
+
+def test_no_rows_and_no_used_experts():
+    a, w = _operands(10, 3, 64, 64, 1)
+    off = torch.zeros(4, dtype=torch.int32, device="cuda")
+    assert stm.mx4_grouped_matmul(stm.Mx4(a.data[:0], a.scale[:0]), w, off).shape == (0, 64)
+    assert stm.mx4_grouped_gate_up(stm.Mx4(a.data[:0], a.scale[:0]), w, off, quantize=True).shape == (0, 32)
+    assert stm.mx4_grouped_matmul(a, w, off).shape == (10, 64)  # nothing to compute
+    torch.cuda.synchronize()
+
+
+# ---- the layer --------------------------------------------------------------
+
+LAYERS = {
+    "qwen3": reduced(CONFIGS["qwen3_30b_a3b"], T=300, H=320, I=224),
+    "zipf": reduced(CONFIGS["deepseek_v2_lite_zipf"], T=512, H=256, I=160, I_shared=272),
+    "dsv4": reduced(CONFIGS["dsv4_flash_ablation"], T=384, H=512, I=256, I_shared=256),
+    "decode": reduced(CONFIGS["decode_weight_streaming"], T=16, H=1024, I=256, I_shared=256),
+    "one_token": reduced(CONFIGS["decode_weight_streaming"], T=1, H=544, I=96, I_shared=64),
+}
+
+
+def _layer(name):
+    cfg = LAYERS[name]
+    dev = {k: (v.cuda() if v is not None else None) for k, v in workloads.generate(cfg, "cpu").items()}
+    p = stm.Problem.from_config(cfg)
+    return p, dev, stm.Mx4SparseMoE(p, dev)
+
+
+@pytest.mark.parametrize("name", list(LAYERS))
+def test_layer(name):
+    """Each stage of the layer in 64 bits, on the 4-bit values that the stage
+    before it produced (a value next to a rounding border may fall on either
+    side, so the chain is checked stage by stage)."""
+    p, dev, moe = _layer(name)
+    x = dev["x"]
+    out, rw, sel = moe(x)
+    assert moe.read_device_error() == 0
+    full = stm.SparseMoE(p, dev)
+    out16, rw16, sel16 = full(x)
+    assert torch.equal(rw, rw16) and torch.equal(sel, sel16)
+    assert torch.equal(moe.forward_counts(), torch.bincount(sel.reshape(-1), minlength=p.E).int())
+
+    plan = stm.dispatch(p, sel)
+    off = plan["offsets"]
+    rows = stm.mx4_permute_rows(p, x, plan)
+    v, _ = ref_quantize(x.cpu())
+    pos = plan["pair_pos"].long().reshape(p.T, p.k)
+    assert same(ref_values(rows)[pos].cpu(), v[:, None].expand(-1, p.k, -1))
+    gu, dn = moe.w["gate_up"], moe.w["down"]
+    h = stm.mx4_grouped_gate_up(rows, gu, off, quantize=True)
+    y, _ = _product(rows, gu, off.cpu())
+    g, u = y[:, : p.I], y[:, p.I:]
+    near = torch.linalg.norm(ref_values(h) - g * torch.sigmoid(g) * u) / torch.linalg.norm(g * torch.sigmoid(g) * u)
+    assert float(near) <= 0.25  # a 4-bit rounding is off by at most a quarter of a value in [4, 8) / 4 ... 6
+    yd, ymag = _product(h, dn, off.cpu())
+    shared = torch.zeros(p.T, p.H, dtype=torch.float32, device="cuda")
+    if p.shared != "none":
+        gamma = torch.sigmoid(x.double() @ dev["shared_gate"].double()).float() if p.shared == "sigmoid_gated" else None
+        shared = stm.shared_expert(p, x, dev["shared_gate_up"], dev["shared_down"], gamma)
+    ref = (yd[pos] * rw.double()[:, :, None]).sum(1) + shared.double()
+    slack = ((_steps(p.I) * ymag[pos] + 2.0 ** -8 * yd[pos].abs()) * rw.double()[:, :, None]).sum(1)
+    # (the gate's own fp32 rounding enters the gated shared expert)
+    slack = slack + 2.0 ** -8 * ref.abs() + 2.0 ** -16 * shared.double().abs()
+    assert bool(((out.double() - ref).abs() <= slack * (1 + 2.0 ** -7)).all())
+    # and 4 bits stay near the bf16 layer: W and x each off by up to 1/4 in the worst value, about 0.1 in the mean
+    rel = float(torch.linalg.norm(out.double() - out16.double()) / torch.linalg.norm(out16.double()))
+    assert rel <= 0.5
+
+
+def test_layer_in_a_graph_and_in_the_host_pipeline():
+    p, dev, moe = _layer("dsv4")
+    x = dev["x"].clone()
+    g = stm.GraphedForward(moe, x)
+    pipe = stm.HostPipeline(moe, depth=2)
+    for seed in (5, 6, 7):
+        batch = _rand((p.T, p.H), seed=seed)
+        x.copy_(batch)
+        got = [t.clone() for t in g.replay()]
+        want = moe(batch)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        host_in, host_out = batch.cpu().pin_memory(), torch.empty(p.T, p.H, dtype=torch.bfloat16).pin_memory()
+        pipe.submit(host_in, host_out)
+        pipe.synchronize()
+        assert torch.equal(host_out, want[0].cpu())
+
+
+def test_layer_with_the_balancer_and_given_outputs():
+    p, dev, moe = _layer("dsv4")
+    bal = stm.BiasBalancer(moe, 1e-3)
+    out = torch.empty(p.T, p.H, dtype=torch.bfloat16, device="cuda")
+    got, rw, sel = moe(dev["x"], out=out)
+    assert got is out
+    bal.stash()
+    before = dev["bias"].clone()
+    bal.update()
+    load = torch.bincount(sel.reshape(-1), minlength=p.E).double()
+    step = torch.sign(load.mean() - load).float() * 1e-3
+    assert torch.allclose(dev["bias"], before + step, atol=1e-7)
+    again = stm.Mx4SparseMoE(p, moe.w)  # weights that are 4 bits already
+    assert again.w["gate_up"] is moe.w["gate_up"]
+    assert torch.equal(again(dev["x"])[1], moe(dev["x"])[1])
+
+
+def test_trained_rows_then_served_in_4_bits():
+    """The operators together: a step of training through permute_rows and
+    unpermute_rows, its weights quantised, and the same tokens served."""
+    p = stm.Problem(T=64, H=64, E=4, k=2, I=64)
+    g = torch.Generator().manual_seed(0)
+    x = torch.randn(p.T, p.H, generator=g).bfloat16().cuda()
+    gate_w = (torch.randn(p.E, p.H, generator=g) / 8).bfloat16().cuda()
+    gu = (torch.randn(p.E, 2 * p.I, p.H, generator=g) / 8).cuda().requires_grad_(True)
+    dn = (torch.randn(p.E, p.H, p.I, generator=g) / 8).cuda().requires_grad_(True)
+    rw, sel, _ = stm.route(p, x, gate_w)
+    plan = stm.dispatch(p, sel)
+    off = plan["offsets"].tolist()
+
+    def experts(rows):
+        ys = []
+        for e in range(p.E):
+            gate, up = (rows[off[e]:off[e + 1]].float() @ gu[e].T).chunk(2, 1)
+            ys.append((torch.nn.functional.silu(gate) * up) @ dn[e].T)
+        return torch.cat(ys)
+
+    out = stm.unpermute_rows(p, experts(stm.permute_rows(p, x, plan)), plan, rw)
+    out.float().square().mean().backward()
+    assert all(bool(torch.isfinite(t.grad).all()) and float(t.grad.abs().sum()) > 0 for t in (gu, dn))
+    with torch.no_grad():
+        gu -= 0.1 * gu.grad
+        dn -= 0.1 * dn.grad
+        plain = stm.unpermute_rows(p, experts(stm.permute_rows(p, x, plan)), plan, rw)
+    served, rw4, sel4 = stm.Mx4SparseMoE(p, {"gate_w": gate_w, "gate_up": gu.detach().bfloat16(),
+                                             "down": dn.detach().bfloat16()})(x)
+    assert torch.equal(sel4, sel) and torch.equal(rw4, rw)
+    assert float(torch.linalg.norm(served.float() - plain.float()) / torch.linalg.norm(plain.float())) <= 0.5
+
+
+def test_refusals():
+    x = _rand((4, 64))
+    q = stm.mx4_quantize(x)
+    w = stm.mx4_quantize(_rand((2, 64, 64)))
+    off = torch.tensor([0, 2, 4], dtype=torch.int32, device="cuda")
+    short = stm.Mx4(q.data, q.scale[:, :8].contiguous())
+    p = stm.Problem(T=4, H=64, E=2, k=1, I=32)
+    plan = stm.dispatch(p, torch.zeros(4, 1, dtype=torch.int64, device="cuda"))
+    bad = [lambda: stm.mx4_quantize(x.half()), lambda: stm.mx4_quantize(x.cpu()), lambda: stm.mx4_quantize(x[:, :48].contiguous()),
+           lambda: stm.mx4_quantize(x.t()), lambda: stm.mx4_quantize(x[0, 0]), lambda: stm.mx4_dequantize(short),
+           lambda: stm.mx4_dequantize(q, torch.float16), lambda: stm.mx4_dequantize(q.data),
+           lambda: stm.mx4_grouped_matmul(short, w, off), lambda: stm.mx4_grouped_matmul(q, q, off),
+           lambda: stm.mx4_grouped_matmul(q, w, off[:2]), lambda: stm.mx4_grouped_matmul(q, w, off.long()),
+           lambda: stm.mx4_grouped_matmul(q, w, off, torch.float16),
+           lambda: stm.mx4_grouped_matmul(q, w, off, ws=torch.zeros(16, device="cuda")),
+           lambda: stm.mx4_grouped_matmul(q, stm.mx4_quantize(_rand((2, 64, 96))), off),
+           lambda: stm.mx4_grouped_gate_up(q, stm.mx4_quantize(_rand((2, 96, 64))), off),
+           lambda: stm.mx4_permute_rows(p, x.float(), plan),
+           lambda: stm.Mx4SparseMoE(stm.Problem(T=4, H=64, E=2, k=1, I=32, dtype="f32"), {}),
+           lambda: stm.Mx4SparseMoE(stm.Problem(T=4, H=64, E=2, k=1, I=40), {})]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+            pytest.fail(f"call {i} was not refused")
+    with pytest.raises(stm.MoeError):  # N not a multiple of 8
+        stm.mx4_grouped_matmul(q, stm.mx4_quantize(_rand((2, 60, 64))), off)
