@@ -57,30 +57,39 @@ constexpr int BK = 256;              // values per step: 128 data bytes, one swi
 constexpr int UNIT = 64;             // B rows per unit
 constexpr int MAX_UNITS = 3;
 constexpr int A_BYTES = BM * BK / 2;
-constexpr int A_BOX_BYTES = 32 * BK / 2;
+constexpr int A_BOX_ROWS = 32;       // rows of the small A box (a short tile loads only those it needs)
 constexpr int UNIT_BYTES = UNIT * BK / 2;
-constexpr int SF_ATOM_BYTES = 512;   // scale words of 128 rows for 128 values of K
-constexpr int SFA_BYTES = 2 * SF_ATOM_BYTES;
+// Scales: a row's 16-byte vector covers 512 values of K, two steps.
+constexpr int SF_ATOM_BYTES = 512;   // scale words of 128 rows for 128 values of K; a vector has four
 constexpr int MAX_STAGES = 8;
-constexpr int ACC_COLS = MAX_UNITS * UNIT;       // TMEM columns of one accumulator
-constexpr int SF_COL = 2 * ACC_COLS;             // two sets of scale columns follow
-constexpr int SF_SET_COLS = 2 * 4 + 2 * 8;       // two atoms of A, two of B (up to 256 rows)
+constexpr int MAX_SF_STAGES = 4;
+constexpr int ACC_COLS = MAX_UNITS * UNIT;         // TMEM columns of one accumulator
+constexpr int SF_COL = 2 * ACC_COLS;               // two sets of scale columns follow
+constexpr int SFB_COL = 4 * 4;                     // in a set: four atoms of A, then four of B (up to 256 rows)
+constexpr int SF_SET_COLS = SFB_COL + 4 * 8;
 constexpr int TMEM_COLS = 512;
 static_assert(SF_COL + 2 * SF_SET_COLS <= TMEM_COLS, "accumulators and scales fit TMEM");
-constexpr int GTHREADS = 256;
-constexpr int STAGING_BYTES = 32 * 64;           // per epilogue warp
+constexpr int EPI_WARP0 = 4;
+constexpr int GTHREADS = 32 * (EPI_WARP0 + 8);
 
-__host__ __device__ constexpr int sfb_blocks(int units) { return (units * UNIT + 127) / 128; }
-__host__ __device__ constexpr int stage_bytes(int units) {
-  return A_BYTES + units * UNIT_BYTES + SFA_BYTES + 2 * sfb_blocks(units) * SF_ATOM_BYTES;
-}
+__host__ __device__ constexpr int stage_bytes(int units) { return A_BYTES + units * UNIT_BYTES; }
 constexpr int RING_BYTES = 5 * stage_bytes(3);
 __host__ __device__ constexpr int ring_stages(int units) {
   return RING_BYTES / stage_bytes(units) < MAX_STAGES ? RING_BYTES / stage_bytes(units) : MAX_STAGES;
 }
+__host__ __device__ constexpr int sfb_blocks(int units) { return (units * UNIT + 127) / 128; }
+__host__ __device__ constexpr int sf_stage_bytes(int units) { return 4 * (1 + sfb_blocks(units)) * SF_ATOM_BYTES; }
+constexpr int SF_RING_BYTES = 3 * sf_stage_bytes(3);
+__host__ __device__ constexpr int sf_stages(int units) { return SF_RING_BYTES / sf_stage_bytes(units); }
+static_assert(sf_stages(1) <= MAX_SF_STAGES && sf_stages(2) <= MAX_SF_STAGES, "scale barriers");
 
 enum { OUT_BF16 = 0, OUT_F32 = 1, SWIGLU_BF16 = 2, SWIGLU_MX4 = 3 };
 constexpr bool is_swiglu(int mode) { return mode >= SWIGLU_BF16; }
+
+struct Maps {
+  CUtensorMap a_box, a_tile;  // A in boxes of 32 rows, and of 128
+  CUtensorMap b[MAX_UNITS];   // W in boxes of 1..3 units
+};
 
 struct Args {
   const int32_t* offsets;
@@ -97,12 +106,15 @@ struct Args {
   void* out;         // bf16 / fp32 [rows, N], or data bytes [rows, N/2]
   uint8_t* out_scale;
   int32_t out_pitch;
+  bool out32;        // out and its rows are 32-byte aligned
   int32_t* err;
 };
 
 struct __align__(8) Ctl {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
+  uint64_t sfull[MAX_SF_STAGES];
+  uint64_t sempty[MAX_SF_STAGES];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;
@@ -113,7 +125,7 @@ struct __align__(8) Ctl {
   int pre[kMaxExperts + 1];
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)RING_BYTES + 4 * STAGING_BYTES + sizeof(Ctl);
+constexpr size_t kSmemBytes = 1024 + (size_t)RING_BYTES + SF_RING_BYTES + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // Instruction descriptor, kind::mxf4: A and B e2m1 (bits 7-9, 10-12 = 1), K
@@ -147,6 +159,21 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t b
 
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// One lane of a converged warp. The tensor-core and TMA instructions take
+// their operands from uniform registers; issued by a lane of a warp that has
+// diverged (`if (lane == 0)` around the whole loop) each of them took about 100
+// clocks, 1050 for a step that now takes 180.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// mbar_wait of a whole warp, which stays converged.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, int32_t* err, int site) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
+}
+
 // Units per tile: the fewest rounds of tiles over the grid, each weighed by the
 // operand bytes of its tiles (8 KB a unit and step, 4 KB for each 32 rows of A
 // that the average tile has). Few row tiles take narrow tiles, so that every
@@ -167,53 +194,69 @@ __device__ __forceinline__ int choose_units(int row_tiles, int rows, int n_units
 }
 
 struct Tile {
-  int e, row0, row_end, unit0, units;
+  int e, row0, row_end, unit0;
 };
 
-__device__ __forceinline__ Tile decode(const Ctl* ctl, const Args& a, int units, int n_tiles, int tile) {
+// The tile's place; e is the expert of an earlier tile of the same CTA (row
+// tiles come in rising order).
+__device__ __forceinline__ Tile decode(const Ctl* ctl, int units, int n_tiles, int tile, int e) {
   Tile t;
   const int mt = tile / n_tiles;
   t.unit0 = (tile - mt * n_tiles) * units;
-  t.units = min(units, a.n_units - t.unit0);
-  t.e = find_segment(ctl->pre, a.E, mt);
-  t.row0 = ctl->off[t.e] + (mt - ctl->pre[t.e]) * BM;
-  t.row_end = ctl->off[t.e + 1];
+  while (ctl->pre[e + 1] <= mt) ++e;
+  t.e = e;
+  t.row0 = ctl->off[e] + (mt - ctl->pre[e]) * BM;
+  t.row_end = ctl->off[e + 1];
   return t;
 }
 
-// One lane's four 16-byte pieces of a 64-byte row piece into the warp's staging
-// buffer (row = lane), then out again as 16-byte stores of whole row pieces,
-// four lanes to a row. A piece's place in its row is rotated by the row, so
-// that neither side has bank conflicts.
-__device__ __forceinline__ void store_rows64(const uint4 (&v)[4], uint8_t* stage, uint8_t* out, int64_t row_bytes,
-                                             int nrows, int bytes, int lane) {
-  __syncwarp();
-#pragma unroll
-  for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(stage + lane * 64 + 16 * (c ^ ((lane >> 1) & 3))) = v[c];
-  __syncwarp();
-  const int c = lane & 3;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = i * 8 + (lane >> 2);
-    const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 64 + 16 * (c ^ ((r >> 1) & 3)));
-    if (r < nrows && c * 16 < bytes) *reinterpret_cast<uint4*>(out + r * row_bytes + c * 16) = w;
+// silu(g) = g / (1 + 2^(-g log2 e)). The product with log2 e is carried in two
+// parts (its rounding would grow with |g|); clamping g to +-88 there keeps
+// 1 + 2^t finite and changes silu by less than 2^-119 |g|. Off by at most 2^-21
+// of the value. (Division and expf cost a slow path on zeros and tiny values,
+// which the rows past a segment hold: 60 thousand clocks a tile.)
+__device__ __forceinline__ float silu(float g) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  constexpr float kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
+  const float x = -fminf(fmaxf(g, -88.f), 88.f);
+  const float t = x * kLog2e;
+  const float low = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  e = fmaf(e, low * 0.6931471805599453f, e);
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return g * r;
+}
+
+// 32 bytes of one lane's row.
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&v)[8], bool aligned32) {
+  if (aligned32) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
   }
 }
 
 template <int MODE>
-__global__ void __launch_bounds__(GTHREADS, 1)
-    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const Args args) {
+__global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* staging = base + RING_BYTES;
-  Ctl* ctl = reinterpret_cast<Ctl*>(staging + 4 * STAGING_BYTES);
+  uint8_t* sf_base = base + RING_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(sf_base + SF_RING_BYTES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
-      mbar_init(&ctl->full[s], 3);  // TMA, and the two scale warps
+      mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
+    }
+    for (int s = 0; s < MAX_SF_STAGES; ++s) {
+      mbar_init(&ctl->sfull[s], 2);  // the two scale warps
+      mbar_init(&ctl->sempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&ctl->tfull[a], 1);
@@ -240,202 +283,259 @@ __global__ void __launch_bounds__(GTHREADS, 1)
   const int units = ctl->units;
   const int n_tiles = (args.n_units + units - 1) / units;
   const int total = ctl->pre[args.E] * n_tiles;
-  const int stages = ring_stages(units), sbytes = stage_bytes(units);
-  const int sfa_off = A_BYTES + units * UNIT_BYTES, sfb_off = sfa_off + SFA_BYTES;
   const int blocks = sfb_blocks(units);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, last_parity = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = decode(ctl, args, units, n_tiles, tile);
-        const int boxes = min(4, (t.row_end - t.row0 + 31) / 32);
-        for (int kt = 0; kt < args.k_steps; ++kt) {
-          if (!mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
-            ok = false;
-            break;
-          }
+    // ---------------- TMA producer ----------------
+    const int stages = ring_stages(units), sbytes = stage_bytes(units);
+    int stage = 0, e = 0;
+    uint32_t phase = 0, issued = 0, last_parity = 0;
+    bool ok = true;
+    const bool elected = elect_one();
+    const CUtensorMap* tmB = &maps.b[units - 1];
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const Tile t = decode(ctl, units, n_tiles, tile, e);
+      e = t.e;
+      const int boxes = (t.row_end - t.row0 + A_BOX_ROWS - 1) / A_BOX_ROWS;
+      const bool whole = boxes >= BM / A_BOX_ROWS;
+      const uint32_t bytes = (uint32_t)((whole ? A_BYTES : boxes * (A_BYTES * A_BOX_ROWS / BM)) + units * UNIT_BYTES);
+      const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT);
+      for (int kt = 0; kt < args.k_steps; ++kt) {
+        if (!warp_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
+          ok = false;
+          break;
+        }
+        if (elected) {
           uint8_t* sa = base + stage * sbytes;
-          mbar_arrive_expect_tx(&ctl->full[stage], (uint32_t)(boxes * A_BOX_BYTES + t.units * UNIT_BYTES));
           const int kb = kt * (BK / 2);
-          for (int i = 0; i < boxes; ++i)
-            tma_load_2d(sa + i * A_BOX_BYTES, &tmA, &ctl->full[stage], kb, t.row0 + 32 * i);
-          for (int j = 0; j < t.units; ++j)
-            tma_load_4d(sa + A_BYTES + j * UNIT_BYTES, &tmB, &ctl->full[stage], kb,
-                        (t.unit0 + j) * (is_swiglu(MODE) ? UNIT / 2 : UNIT), 0, t.e);
-          issued |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
+          mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+          tma_load_4d(sa + A_BYTES, tmB, &ctl->full[stage], kb, n0, 0, t.e);
+          if (whole) {
+            tma_load_2d(sa, &maps.a_tile, &ctl->full[stage], kb, t.row0);
+          } else {
+            for (int i = 0; i < boxes; ++i)
+              tma_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, &ctl->full[stage], kb,
+                          t.row0 + A_BOX_ROWS * i);
           }
         }
+        __syncwarp();
+        issued |= 1u << stage;
+        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
       }
-      // Every copy has landed before the CTA may exit. The full barrier of a
-      // stage also counts the scale warps' arrivals, which make every stage
-      // they can reach unless the kernel gives up.
-      for (int s = 0; s < stages; ++s)
-        if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
     }
+    // Every copy has landed before the CTA may exit.
+    for (int s = 0; s < stages; ++s)
+      if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
+    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ---------------- MMA issuer ----------------
-      int stage = 0, acc = 0, set = 0;
-      uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = decode(ctl, args, units, n_tiles, tile);
-        if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
-        tc_fence_after();
-        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-        const uint32_t idesc0 = make_idesc_mxf4(t.units * UNIT, 0), idesc2 = make_idesc_mxf4(t.units * UNIT, 2);
-        for (int kt = 0; kt < args.k_steps; ++kt) {
-          if (!mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
+    // ---------------- MMA issuer ----------------
+    const int stages = ring_stages(units), sbytes = stage_bytes(units);
+    const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
+    const uint32_t smem_base = smem_u32(base), sf_smem = smem_u32(sf_base);
+    const uint32_t idesc0 = make_idesc_mxf4(units * UNIT, 0), idesc2 = make_idesc_mxf4(units * UNIT, 2);
+    const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
+    int stage = 0, sf_stage = 0, acc = 0, set = 0;
+    uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+    bool ok = true;
+    const bool elected = elect_one();
+    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      if (!warp_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
+      tc_fence_after();
+      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+      uint32_t sfa = 0, sfb = 0;
+      for (int kt = 0; kt < args.k_steps; ++kt) {
+        if ((kt & 1) == 0) {
+          // The scales of two steps to TMEM. The tensor core takes copies and
+          // MMAs in the order of their issue; the other set is still in use.
+          if (!warp_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 8)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_u32(base + stage * sbytes);
-          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS, sfb = sfa + 8;
+          sfa = tmem_base + SF_COL + set * SF_SET_COLS;
+          sfb = sfa + SFB_COL;
+          if (elected) {
+            const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes), db = da + 4 * (SF_ATOM_BYTES / 16);
 #pragma unroll
-          for (int atom = 0; atom < 2; ++atom) {
-            copy_scales(sfa + 4 * atom, sf_desc(sa + sfa_off + atom * SF_ATOM_BYTES));
-            for (int b = 0; b < blocks; ++b)
-              copy_scales(sfb + 8 * atom + 4 * b, sf_desc(sa + sfb_off + (atom * blocks + b) * SF_ATOM_BYTES));
+            for (int i = 0; i < 4; ++i) copy_scales(sfa + 4 * i, da + i * (SF_ATOM_BYTES / 16));
+            if (blocks == 1) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) copy_scales(sfb + 8 * i, db + i * (SF_ATOM_BYTES / 16));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) copy_scales(sfb + 4 * i, db + i * (SF_ATOM_BYTES / 16));
+            }
+            umma_commit(&ctl->sempty[sf_stage]);
           }
-          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
-          const int left = (args.K - kt * BK + 63) / 64;  // 64-value pieces of K left
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (kk < left)
-              umma_mxf4(d_tmem, adesc + 2 * kk, bdesc + 2 * kk, (kk & 1) ? idesc2 : idesc0, sfa + 4 * (kk >> 1),
-                        sfb + 8 * (kk >> 1), (kt > 0 || kk > 0) ? 1u : 0u);
-          umma_commit(&ctl->empty[stage]);
+          __syncwarp();
           set ^= 1;
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
+          if (++sf_stage == sf_count) {
+            sf_stage = 0;
+            sf_phase ^= 1u;
+          }
+        } else {
+          sfa += 2 * 4;
+          sfb += 2 * 8;
+        }
+        if (!warp_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elected) {
+          const uint32_t sa = smem_base + stage * sbytes;
+          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
+          const int left = kt + 1 < args.k_steps ? BK : k_tail;
+          umma_mxf4(d_tmem, adesc, bdesc, idesc0, sfa, sfb, kt > 0 ? 1u : 0u);
+          if (left > 64) umma_mxf4(d_tmem, adesc + 2, bdesc + 2, idesc2, sfa, sfb, 1u);
+          if (left > 128) umma_mxf4(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 8, 1u);
+          if (left > 192) umma_mxf4(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 8, 1u);
+          umma_commit(&ctl->empty[stage]);
+        }
+        __syncwarp();
+        if (++stage == stages) {
+          stage = 0;
+          phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      if (elected) umma_commit(&ctl->tfull[acc]);
+      __syncwarp();
+      acc ^= 1;
+      if (acc == 0) acc_phase ^= 1u;
+    }
+    __syncwarp();
+    if (elected) umma_commit(&ctl->drain);
+    __syncwarp();
+    mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
+    __syncwarp();
+  } else if (warp < EPI_WARP0) {
+    // ---------------- scale producers (warp 2: A, warp 3: B) ----------------
+    // Two vectors are loaded ahead of the one that is stored, across tiles.
+    constexpr int kSlots = MAX_UNITS * UNIT / 32;  // rows of a lane; A has 4
+    const bool is_b = warp == 3;
+    const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
+    const int n_vec = (args.k_steps + 1) / 2;
+    int tile = blockIdx.x, kv = n_vec, e = 0;  // the next vector to load; kv == n_vec: the tile is not set up yet
+    const uint4* src[kSlots];  // this lane's rows' scales, nullptr for a row that the tile lacks
+    auto load = [&](uint4 (&v)[kSlots]) -> int {
+      if (tile >= total) return -1;
+      if (kv == n_vec) {
+        kv = 0;
+        const Tile t = decode(ctl, units, n_tiles, tile, e);
+        e = t.e;
+        if (is_b) {
+          const uint8_t* w = args.b_scale + (int64_t)e * args.b_rows * args.pitch;
+#pragma unroll
+          for (int c = 0; c < kSlots; ++c) {
+            // gate_up: the tile's gate rows, 32 a unit, then its up rows
+            const int up = is_swiglu(MODE) && c >= units ? 1 : 0;
+            const int n = is_swiglu(MODE) ? (t.unit0 + c - up * units) * 32 + lane : t.unit0 * UNIT + 32 * c + lane;
+            const int64_t row = (int64_t)up * args.N + n;
+            src[c] = c < 2 * units && n < args.N ? reinterpret_cast<const uint4*>(w + row * args.pitch) : nullptr;
+          }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kSlots; ++c) {
+            const int row = t.row0 + 32 * c + lane;
+            src[c] = c < 4 && row < t.row_end
+                         ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch)
+                         : nullptr;
           }
         }
-        if (!ok) break;
-        umma_commit(&ctl->tfull[acc]);
-        acc ^= 1;
-        if (acc == 0) acc_phase ^= 1u;
       }
-      umma_commit(&ctl->drain);
-      mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
-    }
-  } else if (warp < 4) {
-    // ---------------- scale producers (warp 2: A, warp 3: B) ----------------
-    constexpr int kMaxRows = MAX_UNITS * UNIT / 32;  // row slots of a lane, A has 4
-    const bool is_b = warp == 3;
+#pragma unroll
+      for (int c = 0; c < kSlots; ++c) v[c] = src[c] ? __ldg(src[c] + kv) : make_uint4(0, 0, 0, 0);
+      const int at = kv;
+      if (++kv == n_vec) tile += gridDim.x;
+      return at;
+    };
     int stage = 0;
     uint32_t phase = 0;
-    bool ok = true;
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      const Tile t = decode(ctl, args, units, n_tiles, tile);
-      const uint4* src[kMaxRows];  // this lane's rows' scales, nullptr for a row that the tile lacks
-      if (is_b) {
-        const uint8_t* w = args.b_scale + (int64_t)t.e * args.b_rows * args.pitch;
+    auto publish = [&](const uint4 (&v)[kSlots], int at) -> bool {
+      if (!warp_wait(&ctl->sempty[stage], phase ^ 1u, &ctl->abort, args.err, 5)) return false;
+      uint8_t* dst = sf_base + stage * sf_bytes + (is_b ? 4 * SF_ATOM_BYTES : 0) + lane * 16;
 #pragma unroll
-        for (int c = 0; c < kMaxRows; ++c) {
-          // gate_up: the unit's 32 gate rows, then its 32 up rows
-          const int n = is_swiglu(MODE) ? (t.unit0 + (c >> 1)) * 32 + lane : t.unit0 * UNIT + 32 * c + lane;
-          const int64_t row = is_swiglu(MODE) ? (int64_t)(c & 1) * args.N + n : n;
-          src[c] = c < 2 * t.units && n < args.N ? reinterpret_cast<const uint4*>(w + row * args.pitch) : nullptr;
-        }
-      } else {
-#pragma unroll
-        for (int c = 0; c < kMaxRows; ++c) {
-          const int row = t.row0 + 32 * c + lane;
-          src[c] = c < 4 && row < t.row_end
-                       ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch)
-                       : nullptr;
+      for (int atom = 0; atom < 4; ++atom) {
+        // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
+        const int valid = args.K / mx4::kBlock - at * 16 - atom * 4;
+        const uint32_t mask = valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
+        auto word = [&](int c) {
+          return mask & (atom == 0 ? v[c].x : atom == 1 ? v[c].y : atom == 2 ? v[c].z : v[c].w);
+        };
+        const uint4 lo = make_uint4(word(0), word(1), word(2), word(3));
+        if (is_b && blocks == 2) {
+          *reinterpret_cast<uint4*>(dst + 2 * atom * SF_ATOM_BYTES) = lo;
+          *reinterpret_cast<uint4*>(dst + (2 * atom + 1) * SF_ATOM_BYTES) = make_uint4(word(4), word(5), 0u, 0u);
+        } else {
+          *reinterpret_cast<uint4*>(dst + atom * SF_ATOM_BYTES) = lo;
         }
       }
-      uint4 next[kMaxRows];
-#pragma unroll
-      for (int c = 0; c < kMaxRows; ++c) next[c] = src[c] ? __ldg(src[c]) : make_uint4(0, 0, 0, 0);
-      for (int kt = 0; ok && kt < args.k_steps; kt += 2) {
-        uint4 v[kMaxRows];
-#pragma unroll
-        for (int c = 0; c < kMaxRows; ++c) v[c] = next[c];
-        if (kt + 2 < args.k_steps) {
-#pragma unroll
-          for (int c = 0; c < kMaxRows; ++c)
-            if (src[c]) next[c] = __ldg(src[c] + (kt >> 1) + 1);
-        }
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (kt + h >= args.k_steps) break;
-          const bool got = mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 5);
-          if (!__all_sync(0xffffffffu, got)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = base + stage * sbytes + (is_b ? sfb_off : sfa_off) + lane * 16;
-          const int nb = is_b ? blocks : 1;
-#pragma unroll
-          for (int atom = 0; atom < 2; ++atom) {
-            // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
-            const int valid = args.K / mx4::kBlock - (kt + h) * 8 - atom * 4;
-            const uint32_t mask = valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-            auto word = [&](int c) {
-              if (c >= kMaxRows) return 0u;
-              const uint4& q = v[c];
-              return mask & (h == 0 ? (atom == 0 ? q.x : q.y) : (atom == 0 ? q.z : q.w));
-            };
-            *reinterpret_cast<uint4*>(dst + atom * nb * SF_ATOM_BYTES) = make_uint4(word(0), word(1), word(2), word(3));
-            if (nb == 2)
-              *reinterpret_cast<uint4*>(dst + (atom * nb + 1) * SF_ATOM_BYTES) = make_uint4(word(4), word(5), 0u, 0u);
-          }
-          fence_to_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->full[stage]);
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-        }
+      fence_to_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->sfull[stage]);
+      if (++stage == sf_count) {
+        stage = 0;
+        phase ^= 1u;
       }
+      return true;
+    };
+    uint4 v0[kSlots], v1[kSlots];
+    int at0 = load(v0), at1 = load(v1);
+    while (at0 >= 0) {
+      if (!publish(v0, at0)) break;
+      at0 = load(v0);
+      if (at1 < 0) break;
+      if (!publish(v1, at1)) break;
+      at1 = load(v1);
     }
+    __syncwarp();
   } else {
-    // ---------------- epilogue (warps 4..7) ----------------
+    // ---------------- epilogue: warps 4..7 take the first accumulator's tiles, 8..11 the second's ----------------
     const int quarter = warp & 3;  // TMEM lanes this warp may access
-    uint8_t* stg = staging + quarter * STAGING_BYTES;
-    int acc = 0;
+    const int acc = (warp - EPI_WARP0) >> 2;
+    const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC_COLS);
     uint32_t acc_phase = 0;
-    for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const Tile t = decode(ctl, args, units, n_tiles, tile);
-      if (!__all_sync(0xffffffffu, mbar_wait(&ctl->tfull[acc], acc_phase, &ctl->abort, args.err, 4))) break;
-      tc_fence_after();
+    int e = 0;
+    for (int tile = blockIdx.x + acc * (int)gridDim.x; tile < total; tile += 2 * gridDim.x) {
+      const Tile t = decode(ctl, units, n_tiles, tile, e);
+      e = t.e;
       const int row_w0 = t.row0 + quarter * 32;
-      const int nrows = min(32, t.row_end - row_w0);
-      const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-      if (nrows > 0) {
+      const bool any = row_w0 < t.row_end, mine = row_w0 + lane < t.row_end;
+      const int64_t row = row_w0 + lane;
+      if (!warp_wait(&ctl->tfull[acc], acc_phase, &ctl->abort, args.err, 4)) break;
+      acc_phase ^= 1u;
+      tc_fence_after();
+      if (any) {
+        if constexpr (is_swiglu(MODE)) {
+          const int count = min(units, args.n_units - t.unit0);
 #pragma unroll 1
-        for (int j = 0; j < t.units; ++j) {
-          uint32_t g[32], u[32];
-          tmem_ld32(tbase + j * UNIT, g);
-          tmem_ld32(tbase + j * UNIT + 32, u);
-          tmem_ld_wait_regs(g);
-          tmem_ld_wait_regs(u);
-          if constexpr (is_swiglu(MODE)) {
+          for (int j = 0; j < count; ++j) {
+            uint32_t g[32], u[32];
+            tmem_ld32(tbase + j * 32, g);
+            tmem_ld32(tbase + (units + j) * 32, u);
+            tmem_ld_wait_regs(g);
+            tmem_ld_wait_regs(u);
             const int n0 = (t.unit0 + j) * 32;  // N is a multiple of 32: the block lies inside
             uint32_t h[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              h[i] = pack_bf16x2(silu_f32(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
-                                 silu_f32(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
+              h[i] = pack_bf16x2(silu(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
+                                 silu(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
             if constexpr (MODE == SWIGLU_BF16) {
-              uint4 v[4];
+              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0) * 2;
+              if (mine) {
 #pragma unroll
-              for (int c = 0; c < 4; ++c) v[c] = make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
-              store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + n0) * 2,
-                           (int64_t)args.N * 2, nrows, 64, lane);
+                for (int c = 0; c < 2; ++c) {
+                  const uint32_t v[8] = {h[8 * c],     h[8 * c + 1], h[8 * c + 2], h[8 * c + 3],
+                                         h[8 * c + 4], h[8 * c + 5], h[8 * c + 6], h[8 * c + 7]};
+                  store32(o + 32 * c, v, args.out32);
+                }
+              }
             } else {
               // the lane's own row: 32 values, one scale
               uint32_t m = 0;
@@ -454,8 +554,7 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                 }
                 code[c] = b == mx4::kScaleNaN ? 0u : mx4::pack8(f);
               }
-              if (lane < nrows) {
-                const int64_t row = row_w0 + lane;
+              if (mine) {
                 *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0) / 2) =
                     make_uint4(code[0], code[1], code[2], code[3]);
                 uint8_t* s = args.out_scale + row * args.out_pitch;
@@ -464,40 +563,34 @@ __global__ void __launch_bounds__(GTHREADS, 1)
                   for (int i = args.N / 32; i < args.out_pitch; ++i) s[i] = 0;
               }
             }
-          } else {
-            const int n0 = (t.unit0 + j) * UNIT;
+          }
+        } else {
+          const int n0 = t.unit0 * UNIT;
+          const int count = min(units * UNIT, args.N - n0);
+#pragma unroll 1
+          for (int c0 = 0; c0 < count; c0 += 32) {
+            uint32_t d[32];
+            tmem_ld32(tbase + c0, d);
+            tmem_ld_wait_regs(d);
             if constexpr (MODE == OUT_BF16) {
+              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0 + c0) * 2;
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const int nh = n0 + 32 * half;
-                if (nh >= args.N) break;
-                uint4 v[4];
+              for (int c = 0; c < 2; ++c) {
+                uint32_t v[8];
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  uint32_t p[4];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    p[i] = half == 0 ? pack_bf16x2(__uint_as_float(g[8 * c + 2 * i]), __uint_as_float(g[8 * c + 2 * i + 1]))
-                                     : pack_bf16x2(__uint_as_float(u[8 * c + 2 * i]), __uint_as_float(u[8 * c + 2 * i + 1]));
-                  v[c] = make_uint4(p[0], p[1], p[2], p[3]);
-                }
-                store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + nh) * 2,
-                             (int64_t)args.N * 2, nrows, 2 * (args.N - nh), lane);
+                for (int i = 0; i < 8; ++i)
+                  v[i] = pack_bf16x2(__uint_as_float(d[16 * c + 2 * i]), __uint_as_float(d[16 * c + 2 * i + 1]));
+                const int left = count - c0 - 16 * c;  // N is a multiple of 8
+                if (mine && left >= 16) store32(o + 32 * c, v, args.out32);
+                else if (mine && left > 0) *reinterpret_cast<uint4*>(o + 32 * c) = make_uint4(v[0], v[1], v[2], v[3]);
               }
             } else {
+              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0 + c0) * 4;
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int nh = n0 + 16 * q;
-                if (nh >= args.N) break;
-                uint4 v[4];
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                  const uint32_t* d = q < 2 ? g : u;
-                  const int o = 16 * (q & 1) + 4 * c;
-                  v[c] = make_uint4(d[o], d[o + 1], d[o + 2], d[o + 3]);
-                }
-                store_rows64(v, stg, reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + nh) * 4,
-                             (int64_t)args.N * 4, nrows, 4 * (args.N - nh), lane);
+              for (int c = 0; c < 4; ++c) {
+                const uint32_t v[8] = {d[8 * c],     d[8 * c + 1], d[8 * c + 2], d[8 * c + 3],
+                                       d[8 * c + 4], d[8 * c + 5], d[8 * c + 6], d[8 * c + 7]};
+                if (mine && c0 + 8 * c < count) store32(o + 32 * c, v, args.out32);
               }
             }
           }
@@ -505,8 +598,6 @@ __global__ void __launch_bounds__(GTHREADS, 1)
       }
       tc_fence_before();
       mbar_arrive(&ctl->tempty[acc]);
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
     }
   }
 
@@ -529,21 +620,23 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   const cudaError_t e = set_max_dynamic_smem_once(kernel, (int)kSmemBytes, once, attr);
   if (e != cudaSuccess) return e;
   if (!get_encode()) return cudaErrorNotSupported;
-  CUtensorMap tmA, tmB;
-  {
+  Maps maps;
+  for (int i = 0; i < 2; ++i) {
     const uint64_t dims[2] = {(uint64_t)K / 2, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)K / 2};
-    const uint32_t box[2] = {BK / 2, 32};
-    if (!make_tensor_map_u8(&tmA, a_data, 2, dims, strides, box)) return cudaErrorInvalidValue;
+    const uint32_t box[2] = {BK / 2, (uint32_t)(i == 0 ? A_BOX_ROWS : BM)};
+    if (!make_tensor_map_u8(i == 0 ? &maps.a_box : &maps.a_tile, a_data, 2, dims, strides, box))
+      return cudaErrorInvalidValue;
   }
-  {
+  for (int u = 1; u <= MAX_UNITS; ++u) {
     // W [E][halves][N][K/2]: gate_up's two halves, or one
     const uint64_t halves = is_swiglu(MODE) ? 2 : 1;
     const uint64_t dims[4] = {(uint64_t)K / 2, (uint64_t)N, halves, (uint64_t)E};
     const uint64_t strides[3] = {(uint64_t)K / 2, (uint64_t)N * K / 2, halves * (uint64_t)N * K / 2};
-    const uint32_t box[4] = {BK / 2, (uint32_t)(UNIT / halves), (uint32_t)halves, 1};
-    if (!make_tensor_map_u8(&tmB, w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    const uint32_t box[4] = {BK / 2, (uint32_t)(u * UNIT / halves), (uint32_t)halves, 1};
+    if (!make_tensor_map_u8(&maps.b[u - 1], w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
+  const int64_t row_bytes = MODE == OUT_F32 ? 4 * N : 2 * N;
   Args a{};
   a.offsets = offsets;
   a.E = (int32_t)E;
@@ -559,10 +652,11 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   a.out = out;
   a.out_scale = static_cast<uint8_t*>(out_scale);
   a.out_pitch = (int32_t)mx4::scale_pitch(N);
+  a.out32 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)row_bytes) % 32 == 0;
   a.err = err;
   const int64_t most = (rows / BM + std::min<int64_t>(rows, E)) * a.n_units;  // tiles of one unit
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms(), most));
-  mx4_gemm_kernel<MODE><<<grid, GTHREADS, kSmemBytes, s>>>(tmA, tmB, a);
+  mx4_gemm_kernel<MODE><<<grid, GTHREADS, kSmemBytes, s>>>(maps, a);
   return cudaGetLastError();
 }
 
