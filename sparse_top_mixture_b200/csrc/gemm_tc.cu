@@ -502,24 +502,20 @@ bool get_encode() {
   return g_encode != nullptr;
 }
 
-static bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType type, const void* ptr, int rank,
-                            const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box) {
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* ptr, int rank,
+                     const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box) {
   const uint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r =
       g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(ptr), dims, strides_bytes,
-               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
 
 bool make_tensor_map_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                           const uint64_t* strides_bytes, const uint32_t* box) {
-  return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, ptr, rank, dims, strides_bytes, box);
-}
-
-bool make_tensor_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
-                        const uint64_t* strides_bytes, const uint32_t* box) {
-  return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, ptr, rank, dims, strides_bytes, box);
+  return make_tensor_map(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, CU_TENSOR_MAP_SWIZZLE_128B, ptr, rank, dims,
+                         strides_bytes, box);
 }
 
 int num_sms() {

@@ -167,8 +167,8 @@ int tc_gemm_launches(const Segments& sg);
 bool get_encode();
 bool make_tensor_map_bf16(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
                           const uint64_t* strides_bytes, const uint32_t* box);
-bool make_tensor_map_u8(CUtensorMap* m, const void* ptr, int rank, const uint64_t* dims,
-                        const uint64_t* strides_bytes, const uint32_t* box);
+bool make_tensor_map(CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* ptr, int rank,
+                     const uint64_t* dims, const uint64_t* strides_bytes, const uint32_t* box);
 int num_sms();
 // CTA-pair GEMMs; A is the row-major operand (x_perm or h), the tensor maps
 // are built inside.

@@ -71,9 +71,10 @@ constexpr int TMEM_COLS = 512;
 static_assert(SF_COL + 2 * SF_SET_COLS <= TMEM_COLS, "accumulators and scales fit TMEM");
 constexpr int EPI_WARP0 = 4;
 constexpr int GTHREADS = 32 * (EPI_WARP0 + 8);
+constexpr int STAGING_BYTES = 32 * 128;            // per epilogue warp
 
 __host__ __device__ constexpr int stage_bytes(int units) { return A_BYTES + units * UNIT_BYTES; }
-constexpr int RING_BYTES = 5 * stage_bytes(3);
+constexpr int RING_BYTES = 4 * stage_bytes(3);
 __host__ __device__ constexpr int ring_stages(int units) {
   return RING_BYTES / stage_bytes(units) < MAX_STAGES ? RING_BYTES / stage_bytes(units) : MAX_STAGES;
 }
@@ -89,6 +90,7 @@ constexpr bool is_swiglu(int mode) { return mode >= SWIGLU_BF16; }
 struct Maps {
   CUtensorMap a_box, a_tile;  // A in boxes of 32 rows, and of 128
   CUtensorMap b[MAX_UNITS];   // W in boxes of 1..3 units
+  CUtensorMap out;            // out in a warp's staged boxes
 };
 
 struct Args {
@@ -106,7 +108,6 @@ struct Args {
   void* out;         // bf16 / fp32 [rows, N], or data bytes [rows, N/2]
   uint8_t* out_scale;
   int32_t out_pitch;
-  bool out32;        // out and its rows are 32-byte aligned
   int32_t* err;
 };
 
@@ -125,7 +126,8 @@ struct __align__(8) Ctl {
   int pre[kMaxExperts + 1];
 };
 
-constexpr size_t kSmemBytes = 1024 + (size_t)RING_BYTES + SF_RING_BYTES + sizeof(Ctl);
+static_assert(RING_BYTES % 1024 == 0 && SF_RING_BYTES % 1024 == 0 && STAGING_BYTES % 1024 == 0, "swizzled buffers");
+constexpr size_t kSmemBytes = 1024 + (size_t)RING_BYTES + SF_RING_BYTES + 8 * STAGING_BYTES + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 // Instruction descriptor, kind::mxf4: A and B e2m1 (bits 7-9, 10-12 = 1), K
@@ -160,9 +162,9 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t b
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // One lane of a converged warp. The tensor-core and TMA instructions take
-// their operands from uniform registers; issued by a lane of a warp that has
-// diverged (`if (lane == 0)` around the whole loop) each of them took about 100
-// clocks, 1050 for a step that now takes 180.
+// their operands from uniform registers. In a loop that a lane chosen by number
+// runs (`if (lane == 0)`) each of them took about 100 clocks, 1050 for a step;
+// a lane chosen by elect.sync issues a step in 180.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
@@ -174,6 +176,20 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
 }
 
+// Whether a phase is complete: issued before other work, it hides the 100 clocks
+// that even a wait for a phase long complete takes.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Units per tile: the fewest rounds of tiles over the grid, each weighed by the
 // operand bytes of its tiles (8 KB a unit and step, 4 KB for each 32 rows of A
 // that the average tile has). Few row tiles take narrow tiles, so that every
@@ -181,11 +197,12 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* a
 __device__ __forceinline__ int choose_units(int row_tiles, int rows, int n_units, int grid) {
   const int boxes = row_tiles > 0 ? min(4, (rows / row_tiles + 31) / 32) : 1;
   int best = MAX_UNITS;
-  long long least = -1;
+  uint32_t least = 0xffffffffu;
+#pragma unroll
   for (int u = MAX_UNITS; u >= 1; --u) {
-    const long long tiles = (long long)row_tiles * ((n_units + u - 1) / u);
-    const long long cost = (tiles + grid - 1) / grid * (2 * u + max(1, boxes));
-    if (least < 0 || cost < least) {
+    const uint32_t tiles = (uint32_t)row_tiles * ((uint32_t)(n_units + u - 1) / u);
+    const uint32_t cost = (tiles + grid - 1) / (uint32_t)grid * (2 * u + max(1, boxes));
+    if (cost < least) {
       least = cost;
       best = u;
     }
@@ -228,16 +245,46 @@ __device__ __forceinline__ float silu(float g) {
   return g * r;
 }
 
-// 32 bytes of one lane's row.
-__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&v)[8], bool aligned32) {
-  if (aligned32) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
+// A warp stages boxes of its 32 rows by BYTES (64 or 128) of a row and stores
+// them by TMA, or where the tile has fewer rows by plain stores. The 16-byte
+// piece c of row r is at c ^ (r & 7), or c ^ (r / 2 & 3): the TMA swizzles of
+// these widths, and neither lanes that write their own row nor lanes that read
+// along rows meet in a bank. (Stores straight from the lanes' rows, 32 lines an
+// instruction, bound the product's epilogue; plain stores of staged rows held
+// their warp for about 900 clocks a box.)
+template <int BYTES>
+__device__ __forceinline__ int staged(int r, int c) {
+  return r * BYTES + 16 * (BYTES == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3));
+}
+
+template <int BYTES>
+__device__ __forceinline__ void store_box(const uint8_t* stage, const CUtensorMap* map, int col, int row, uint8_t* out,
+                                          int64_t row_bytes, int nrows, int bytes, int lane) {
+  if (nrows >= 32) {
+    fence_to_async();
+    __syncwarp();
+    if (lane == 0) tma_store_2d(map, stage, col, row);
   } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    __syncwarp();
+    constexpr int kPerRow = BYTES / 16;
+    const int c = lane % kPerRow;
+#pragma unroll
+    for (int i = 0; i < kPerRow; ++i) {
+      const int r = i * (32 / kPerRow) + lane / kPerRow;
+      if (r < nrows && c * 16 < bytes)
+        *reinterpret_cast<uint4*>(out + r * row_bytes + c * 16) =
+            *reinterpret_cast<const uint4*>(stage + staged<BYTES>(r, c));
+    }
+    __syncwarp();
   }
+  if (lane == 0) bulk_commit();  // a box is a group, an empty one where it went out by plain stores
+}
+
+// The buffers of all but the last N boxes may be written again.
+template <int N>
+__device__ __forceinline__ void box_free(int lane) {
+  if (lane == 0) bulk_wait_read<N>();
+  __syncwarp();
 }
 
 template <int MODE>
@@ -245,7 +292,8 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf_base = base + RING_BYTES;
-  Ctl* ctl = reinterpret_cast<Ctl*>(sf_base + SF_RING_BYTES);
+  uint8_t* staging = sf_base + SF_RING_BYTES;
+  Ctl* ctl = reinterpret_cast<Ctl*>(staging + 8 * STAGING_BYTES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
 
@@ -287,25 +335,28 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
-    const int stages = ring_stages(units), sbytes = stage_bytes(units);
-    int stage = 0, e = 0;
-    uint32_t phase = 0, issued = 0, last_parity = 0;
-    bool ok = true;
-    const bool elected = elect_one();
-    const CUtensorMap* tmB = &maps.b[units - 1];
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      const Tile t = decode(ctl, units, n_tiles, tile, e);
-      e = t.e;
-      const int boxes = (t.row_end - t.row0 + A_BOX_ROWS - 1) / A_BOX_ROWS;
-      const bool whole = boxes >= BM / A_BOX_ROWS;
-      const uint32_t bytes = (uint32_t)((whole ? A_BYTES : boxes * (A_BYTES * A_BOX_ROWS / BM)) + units * UNIT_BYTES);
-      const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT);
-      for (int kt = 0; kt < args.k_steps; ++kt) {
-        if (!warp_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
-          ok = false;
-          break;
-        }
-        if (elected) {
+    if (elect_one()) {
+      const int stages = ring_stages(units), sbytes = stage_bytes(units);
+      int stage = 0, e = 0;
+      uint32_t phase = 0, issued = 0, last_parity = 0;
+      bool ok = true;
+      const CUtensorMap* tmB = &maps.b[units - 1];
+      bool seen = false;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        const Tile t = decode(ctl, units, n_tiles, tile, e);
+        e = t.e;
+        const int boxes = (t.row_end - t.row0 + A_BOX_ROWS - 1) / A_BOX_ROWS;
+        const bool whole = boxes >= BM / A_BOX_ROWS;
+        const uint32_t bytes = (uint32_t)((whole ? A_BYTES : boxes * (A_BYTES * A_BOX_ROWS / BM)) + units * UNIT_BYTES);
+        const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT);
+        for (int kt = 0; kt < args.k_steps; ++kt) {
+          if (!seen && !mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
+            ok = false;
+            break;
+          }
+          const int next = stage + 1 == stages ? 0 : stage + 1;
+          const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+          seen = mbar_test(&ctl->empty[next], next_phase ^ 1u);
           uint8_t* sa = base + stage * sbytes;
           const int kb = kt * (BK / 2);
           mbar_arrive_expect_tx(&ctl->full[stage], bytes);
@@ -317,48 +368,44 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
               tma_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, &ctl->full[stage], kb,
                           t.row0 + A_BOX_ROWS * i);
           }
-        }
-        __syncwarp();
-        issued |= 1u << stage;
-        last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
+          issued |= 1u << stage;
+          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
+          stage = next;
+          phase = next_phase;
         }
       }
+      // Every copy has landed before the CTA may exit.
+      for (int s = 0; s < stages; ++s)
+        if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
     }
-    // Every copy has landed before the CTA may exit.
-    for (int s = 0; s < stages; ++s)
-      if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    const int stages = ring_stages(units), sbytes = stage_bytes(units);
-    const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
-    const uint32_t smem_base = smem_u32(base), sf_smem = smem_u32(sf_base);
-    const uint32_t idesc0 = make_idesc_mxf4(units * UNIT, 0), idesc2 = make_idesc_mxf4(units * UNIT, 2);
-    const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
-    int stage = 0, sf_stage = 0, acc = 0, set = 0;
-    uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
-    bool ok = true;
-    const bool elected = elect_one();
-    for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      if (!warp_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-      uint32_t sfa = 0, sfb = 0;
-      for (int kt = 0; kt < args.k_steps; ++kt) {
-        if ((kt & 1) == 0) {
-          // The scales of two steps to TMEM. The tensor core takes copies and
-          // MMAs in the order of their issue; the other set is still in use.
-          if (!warp_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 8)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          sfa = tmem_base + SF_COL + set * SF_SET_COLS;
-          sfb = sfa + SFB_COL;
-          if (elected) {
+    if (elect_one()) {
+      const int stages = ring_stages(units), sbytes = stage_bytes(units);
+      const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
+      const uint32_t smem_base = smem_u32(base), sf_smem = smem_u32(sf_base);
+      const uint32_t idesc0 = make_idesc_mxf4(units * UNIT, 0), idesc2 = make_idesc_mxf4(units * UNIT, 2);
+      const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
+      int stage = 0, sf_stage = 0, acc = 0, set = 0;
+      uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
+      bool ok = true, seen = false, sf_seen = false;
+      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
+        uint32_t sfa = 0, sfb = 0;
+        for (int kt = 0; kt < args.k_steps; ++kt) {
+          if ((kt & 1) == 0) {
+            // The scales of two steps to TMEM. The tensor core takes copies and
+            // MMAs in the order of their issue; the other set is still in use.
+            if (!sf_seen && !mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 8)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            sfa = tmem_base + SF_COL + set * SF_SET_COLS;
+            sfb = sfa + SFB_COL;
             const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes), db = da + 4 * (SF_ATOM_BYTES / 16);
 #pragma unroll
             for (int i = 0; i < 4; ++i) copy_scales(sfa + 4 * i, da + i * (SF_ATOM_BYTES / 16));
@@ -370,23 +417,24 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
               for (int i = 0; i < 8; ++i) copy_scales(sfb + 4 * i, db + i * (SF_ATOM_BYTES / 16));
             }
             umma_commit(&ctl->sempty[sf_stage]);
+            set ^= 1;
+            if (++sf_stage == sf_count) {
+              sf_stage = 0;
+              sf_phase ^= 1u;
+            }
+          } else {
+            sfa += 2 * 4;
+            sfb += 2 * 8;
           }
-          __syncwarp();
-          set ^= 1;
-          if (++sf_stage == sf_count) {
-            sf_stage = 0;
-            sf_phase ^= 1u;
+          if (!seen && !mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
+            ok = false;
+            break;
           }
-        } else {
-          sfa += 2 * 4;
-          sfb += 2 * 8;
-        }
-        if (!warp_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        if (elected) {
+          tc_fence_after();
+          const int next = stage + 1 == stages ? 0 : stage + 1;
+          const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+          seen = mbar_test(&ctl->full[next], next_phase);
+          sf_seen = mbar_test(&ctl->sfull[sf_stage], sf_phase);
           const uint32_t sa = smem_base + stage * sbytes;
           const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
           const int left = kt + 1 < args.k_steps ? BK : k_tail;
@@ -395,23 +443,17 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
           if (left > 128) umma_mxf4(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 8, 1u);
           if (left > 192) umma_mxf4(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 8, 1u);
           umma_commit(&ctl->empty[stage]);
+          stage = next;
+          phase = next_phase;
         }
-        __syncwarp();
-        if (++stage == stages) {
-          stage = 0;
-          phase ^= 1u;
-        }
+        if (!ok) break;
+        umma_commit(&ctl->tfull[acc]);
+        acc ^= 1;
+        if (acc == 0) acc_phase ^= 1u;
       }
-      if (!ok) break;
-      if (elected) umma_commit(&ctl->tfull[acc]);
-      __syncwarp();
-      acc ^= 1;
-      if (acc == 0) acc_phase ^= 1u;
+      umma_commit(&ctl->drain);
+      mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     }
-    __syncwarp();
-    if (elected) umma_commit(&ctl->drain);
-    __syncwarp();
-    mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     __syncwarp();
   } else if (warp < EPI_WARP0) {
     // ---------------- scale producers (warp 2: A, warp 3: B) ----------------
@@ -499,18 +541,19 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int acc = (warp - EPI_WARP0) >> 2;
     const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+    uint8_t* stg = staging + (warp - EPI_WARP0) * STAGING_BYTES;
     uint32_t acc_phase = 0;
     int e = 0;
+    [[maybe_unused]] int other = 0;
     for (int tile = blockIdx.x + acc * (int)gridDim.x; tile < total; tile += 2 * gridDim.x) {
       const Tile t = decode(ctl, units, n_tiles, tile, e);
       e = t.e;
       const int row_w0 = t.row0 + quarter * 32;
-      const bool any = row_w0 < t.row_end, mine = row_w0 + lane < t.row_end;
-      const int64_t row = row_w0 + lane;
+      const int nrows = t.row_end - row_w0;
       if (!warp_wait(&ctl->tfull[acc], acc_phase, &ctl->abort, args.err, 4)) break;
       acc_phase ^= 1u;
       tc_fence_after();
-      if (any) {
+      if (nrows > 0) {
         if constexpr (is_swiglu(MODE)) {
           const int count = min(units, args.n_units - t.unit0);
 #pragma unroll 1
@@ -520,6 +563,10 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
             tmem_ld32(tbase + (units + j) * 32, u);
             tmem_ld_wait_regs(g);
             tmem_ld_wait_regs(u);
+            if (j + 1 == count) {  // the tile's last read
+              tc_fence_before();
+              mbar_arrive(&ctl->tempty[acc]);
+            }
             const int n0 = (t.unit0 + j) * 32;  // N is a multiple of 32: the block lies inside
             uint32_t h[16];
 #pragma unroll
@@ -527,15 +574,16 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
               h[i] = pack_bf16x2(silu(__uint_as_float(g[2 * i])) * __uint_as_float(u[2 * i]),
                                  silu(__uint_as_float(g[2 * i + 1])) * __uint_as_float(u[2 * i + 1]));
             if constexpr (MODE == SWIGLU_BF16) {
-              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0) * 2;
-              if (mine) {
+              uint8_t* box = stg + other;  // two buffers in turn
+              other ^= 32 * 64;
+              box_free<1>(lane);
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  const uint32_t v[8] = {h[8 * c],     h[8 * c + 1], h[8 * c + 2], h[8 * c + 3],
-                                         h[8 * c + 4], h[8 * c + 5], h[8 * c + 6], h[8 * c + 7]};
-                  store32(o + 32 * c, v, args.out32);
-                }
-              }
+              for (int c = 0; c < 4; ++c)
+                *reinterpret_cast<uint4*>(box + staged<64>(lane, c)) =
+                    make_uint4(h[4 * c], h[4 * c + 1], h[4 * c + 2], h[4 * c + 3]);
+              store_box<64>(box, &maps.out, n0, row_w0,
+                            reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + n0) * 2,
+                            (int64_t)args.N * 2, nrows, 64, lane);
             } else {
               // the lane's own row: 32 values, one scale
               uint32_t m = 0;
@@ -554,7 +602,8 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
                 }
                 code[c] = b == mx4::kScaleNaN ? 0u : mx4::pack8(f);
               }
-              if (mine) {
+              if (lane < nrows) {
+                const int64_t row = row_w0 + lane;
                 *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0) / 2) =
                     make_uint4(code[0], code[1], code[2], code[3]);
                 uint8_t* s = args.out_scale + row * args.out_pitch;
@@ -567,38 +616,45 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
         } else {
           const int n0 = t.unit0 * UNIT;
           const int count = min(units * UNIT, args.N - n0);
+          constexpr int kCols = MODE == OUT_BF16 ? 64 : 32;  // 128 bytes of a row
+          constexpr int es = MODE == OUT_BF16 ? 2 : 4;
 #pragma unroll 1
-          for (int c0 = 0; c0 < count; c0 += 32) {
-            uint32_t d[32];
-            tmem_ld32(tbase + c0, d);
-            tmem_ld_wait_regs(d);
+          for (int c0 = 0; c0 < count; c0 += kCols) {
+            uint32_t v[32];
             if constexpr (MODE == OUT_BF16) {
-              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0 + c0) * 2;
 #pragma unroll
-              for (int c = 0; c < 2; ++c) {
-                uint32_t v[8];
+              for (int half = 0; half < 2; ++half) {
+                uint32_t d[32];
+                tmem_ld32(tbase + c0 + half * 32, d);
+                tmem_ld_wait_regs(d);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                  v[i] = pack_bf16x2(__uint_as_float(d[16 * c + 2 * i]), __uint_as_float(d[16 * c + 2 * i + 1]));
-                const int left = count - c0 - 16 * c;  // N is a multiple of 8
-                if (mine && left >= 16) store32(o + 32 * c, v, args.out32);
-                else if (mine && left > 0) *reinterpret_cast<uint4*>(o + 32 * c) = make_uint4(v[0], v[1], v[2], v[3]);
+                for (int i = 0; i < 16; ++i)
+                  v[half * 16 + i] = pack_bf16x2(__uint_as_float(d[2 * i]), __uint_as_float(d[2 * i + 1]));
               }
             } else {
-              uint8_t* o = reinterpret_cast<uint8_t*>(args.out) + (row * args.N + n0 + c0) * 4;
-#pragma unroll
-              for (int c = 0; c < 4; ++c) {
-                const uint32_t v[8] = {d[8 * c],     d[8 * c + 1], d[8 * c + 2], d[8 * c + 3],
-                                       d[8 * c + 4], d[8 * c + 5], d[8 * c + 6], d[8 * c + 7]};
-                if (mine && c0 + 8 * c < count) store32(o + 32 * c, v, args.out32);
-              }
+              tmem_ld32(tbase + c0, v);
+              tmem_ld_wait_regs(v);
             }
+            if (c0 + kCols >= count) {  // the tile's last read
+              tc_fence_before();
+              mbar_arrive(&ctl->tempty[acc]);
+            }
+            box_free<0>(lane);
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              *reinterpret_cast<uint4*>(stg + staged<128>(lane, c)) =
+                  make_uint4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
+            store_box<128>(stg, &maps.out, n0 + c0, row_w0,
+                           reinterpret_cast<uint8_t*>(args.out) + ((int64_t)row_w0 * args.N + n0 + c0) * es,
+                           (int64_t)args.N * es, nrows, min(128, (count - c0) * es), lane);
           }
         }
+      } else {
+        tc_fence_before();
+        mbar_arrive(&ctl->tempty[acc]);
       }
-      tc_fence_before();
-      mbar_arrive(&ctl->tempty[acc]);
     }
+    if constexpr (MODE != SWIGLU_MX4) box_free<0>(lane);
   }
 
   tc_fence_before();
@@ -625,7 +681,8 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
     const uint64_t dims[2] = {(uint64_t)K / 2, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)K / 2};
     const uint32_t box[2] = {BK / 2, (uint32_t)(i == 0 ? A_BOX_ROWS : BM)};
-    if (!make_tensor_map_u8(i == 0 ? &maps.a_box : &maps.a_tile, a_data, 2, dims, strides, box))
+    if (!make_tensor_map(i == 0 ? &maps.a_box : &maps.a_tile, CU_TENSOR_MAP_DATA_TYPE_UINT8,
+                         CU_TENSOR_MAP_SWIZZLE_128B, a_data, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
   for (int u = 1; u <= MAX_UNITS; ++u) {
@@ -634,9 +691,18 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
     const uint64_t dims[4] = {(uint64_t)K / 2, (uint64_t)N, halves, (uint64_t)E};
     const uint64_t strides[3] = {(uint64_t)K / 2, (uint64_t)N * K / 2, halves * (uint64_t)N * K / 2};
     const uint32_t box[4] = {BK / 2, (uint32_t)(u * UNIT / halves), (uint32_t)halves, 1};
-    if (!make_tensor_map_u8(&maps.b[u - 1], w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!make_tensor_map(&maps.b[u - 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const int64_t row_bytes = MODE == OUT_F32 ? 4 * N : 2 * N;
+  if (MODE != SWIGLU_MX4) {
+    const uint64_t es = MODE == OUT_F32 ? 4 : 2;
+    const uint64_t dims[2] = {(uint64_t)N, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)N * es};
+    const uint32_t box[2] = {MODE == OUT_BF16 ? 64u : 32u, 32};
+    if (!make_tensor_map(&maps.out, MODE == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                         MODE == SWIGLU_BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, out, 2, dims,
+                         strides, box))
+      return cudaErrorInvalidValue;
+  }
   Args a{};
   a.offsets = offsets;
   a.E = (int32_t)E;
@@ -652,7 +718,6 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   a.out = out;
   a.out_scale = static_cast<uint8_t*>(out_scale);
   a.out_pitch = (int32_t)mx4::scale_pitch(N);
-  a.out32 = (reinterpret_cast<uintptr_t>(out) | (uintptr_t)row_bytes) % 32 == 0;
   a.err = err;
   const int64_t most = (rows / BM + std::min<int64_t>(rows, E)) * a.n_units;  // tiles of one unit
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms(), most));
