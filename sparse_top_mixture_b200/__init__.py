@@ -12,7 +12,6 @@ Build the library with ``python -m sparse_top_mixture_b200.build``.
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -170,13 +169,21 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _stream(device=None) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+def _stream(device: Optional[torch.device] = None) -> int:
+    index = None if device is None else device.index
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
-def _on(device: torch.device):
-    """Makes ``device`` the current one for a launch on its stream."""
-    return contextlib.nullcontext() if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+def _launch(fn, device: torch.device, *args) -> None:
+    """fn(*args, stream) on device's current stream, with device the current one."""
+    index = device.index
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != 0:
+        _check(status)
 
 
 def _req(t: torch.Tensor, name: str, shape: Sequence[int], dtype: torch.dtype) -> None:
@@ -184,7 +191,7 @@ def _req(t: torch.Tensor, name: str, shape: Sequence[int], dtype: torch.dtype) -
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != (shape if isinstance(shape, tuple) else tuple(shape)):
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")

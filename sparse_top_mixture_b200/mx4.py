@@ -17,14 +17,13 @@ power-of-two scale (``include/moe.h`` gives the format and the rounding).
 
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
-from typing import Dict, Optional, Sequence
+from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
-from . import (DTYPES, TORCH_DTYPE, Problem, SparseMoE, _check, _on, _ptr, _req, _stream, dispatch, lib, new_workspace,
-               route, shared_expert)
+from . import (DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, dispatch, lib, new_workspace, route,
+               shared_expert)
 from .rows import _plan, _same_device, unpermute_rows
 
 _DTYPE_ID = {TORCH_DTYPE[name]: i for name, i in DTYPES.items()}
@@ -62,76 +61,83 @@ def _req_k(K: int, name: str) -> None:
         raise ValueError(f"{name}: the last dimension is {K}, expected a positive multiple of 32")
 
 
-def _req_mx4(q: Mx4, name: str, lead: Optional[Sequence[int]] = None) -> None:
+def _req_mx4(q: Mx4, name: str, lead: Optional[Sequence[int]] = None) -> int:
+    """K of q, which has leading dimensions `lead` (None: any)."""
     if not isinstance(q, Mx4):
         raise ValueError(f"{name} must be an Mx4")
     if not isinstance(q.data, torch.Tensor) or q.data.dim() < 1:
         raise ValueError(f"{name}.data must be a CUDA tensor of at least one dimension")
-    _req_k(q.K, name)
-    lead = tuple(q.data.shape[:-1]) if lead is None else tuple(lead)
-    _req(q.data, f"{name}.data", lead + (q.K // 2,), torch.uint8)
-    _req(q.scale, f"{name}.scale", lead + (_scale_bytes(q.K),), torch.uint8)
-    _same_device(q.data.device, **{f"{name}.scale": q.scale})
+    shape = q.data.shape
+    K = 2 * shape[-1]
+    _req_k(K, name)
+    lead = tuple(shape[:-1] if lead is None else lead)
+    _req(q.data, f"{name}.data", lead + (K // 2,), torch.uint8)
+    _req(q.scale, f"{name}.scale", lead + (_scale_bytes(K),), torch.uint8)
+    if q.scale.get_device() != q.data.get_device():
+        raise ValueError(f"{name}.scale is on {q.scale.device}, expected {q.data.device}")
+    return K
 
 
-def _new(lead: Sequence[int], K: int, device) -> Mx4:
-    return Mx4(torch.empty(*lead, K // 2, dtype=torch.uint8, device=device),
-               torch.empty(*lead, _scale_bytes(K), dtype=torch.uint8, device=device))
+def _new(lead: Tuple[int, ...], K: int, device) -> Mx4:
+    return Mx4(torch.empty(lead + (K // 2,), dtype=torch.uint8, device=device),
+               torch.empty(lead + (_scale_bytes(K),), dtype=torch.uint8, device=device))
 
 
 def mx4_quantize(x: torch.Tensor) -> Mx4:
     """x [..., K] (bf16 or fp32, contiguous, K a multiple of 32) in 4 bits."""
     if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_ID:
         raise ValueError("x must be a bf16 or fp32 CUDA tensor")
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise ValueError("x must have at least one dimension")
-    _req(x, "x", x.shape, x.dtype)
-    K = x.shape[-1]
+    _req(x, "x", shape, x.dtype)
+    K = shape[-1]
     _req_k(K, "x")
-    q = _new(x.shape[:-1], K, x.device)
-    with _on(x.device):
-        _check(lib().moe_mx4_quantize(x.numel() // K, K, _DTYPE_ID[x.dtype], _ptr(x), _ptr(q.data), _ptr(q.scale),
-                                      _stream(x.device)))
+    dev = x.device
+    q = _new(tuple(shape[:-1]), K, dev)
+    _launch(lib().moe_mx4_quantize, dev, x.numel() // K, K, _DTYPE_ID[x.dtype], x.data_ptr(), q.data.data_ptr(),
+            q.scale.data_ptr())
     return q
 
 
 def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     """The values q stands for, [..., K] in bf16 or fp32."""
-    _req_mx4(q, "q")
+    K = _req_mx4(q, "q")
     if dtype not in _DTYPE_ID:
         raise ValueError(f"dtype {dtype}, expected bf16 or fp32")
-    out = torch.empty(q.shape, dtype=dtype, device=q.device)
-    with _on(q.device):
-        _check(lib().moe_mx4_dequantize(out.numel() // q.K, q.K, _DTYPE_ID[dtype], _ptr(q.data), _ptr(q.scale),
-                                        _ptr(out), _stream(q.device)))
+    dev = q.data.device
+    out = torch.empty(q.data.shape[:-1] + (K,), dtype=dtype, device=dev)
+    _launch(lib().moe_mx4_dequantize, dev, out.numel() // K, K, _DTYPE_ID[dtype], q.data.data_ptr(),
+            q.scale.data_ptr(), out.data_ptr())
     return out
 
 
 def mx4_permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]) -> Mx4:
     """``mx4_quantize(permute_rows(p, x, plan))``, each token quantised once:
     [T*k, H] in 4 bits, sorted by expert; rows past the last segment are zeros."""
-    _req(x, "x", (p.T, p.H), p.torch_dtype)
+    _req(x, "x", (p.T, p.H), TORCH_DTYPE[p.dtype])
     _req_k(p.H, "x")
     pair_pos, offsets = _plan(p, plan)
-    _same_device(x.device, pair_pos=pair_pos, offsets=offsets)
-    q = _new((p.T * p.k,), p.H, x.device)
-    with _on(x.device):
-        _check(lib().moe_mx4_permute_rows(ctypes.byref(p.c()), _ptr(x), _ptr(pair_pos), _ptr(offsets), _ptr(q.data),
-                                          _ptr(q.scale), _stream(x.device)))
+    dev = x.device
+    _same_device(dev, pair_pos=pair_pos, offsets=offsets)
+    q = _new((p.T * p.k,), p.H, dev)
+    _launch(lib().moe_mx4_permute_rows, dev, p.c(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(),
+            q.data.data_ptr(), q.scale.data_ptr())
     return q
 
 
-def _req_product(a: Mx4, w: Mx4, offsets, ws) -> None:
-    _req_mx4(a, "a")
-    _req_mx4(w, "w")
+def _req_product(a: Mx4, w: Mx4, offsets, ws) -> int:
+    """K of the product."""
+    K = _req_mx4(a, "a")
+    if _req_mx4(w, "w") != K:
+        raise ValueError(f"a has K {K}, w {w.K}")
     if a.data.dim() != 2 or w.data.dim() != 3:
         raise ValueError("a must be [rows, K] and w [E, N, K]")
-    if a.K != w.K:
-        raise ValueError(f"a has K {a.K}, w {w.K}")
     _req(offsets, "offsets", (w.data.shape[0] + 1,), torch.int32)
     if ws is not None and (not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.numel() * ws.element_size() < 256):
         raise ValueError("ws must be a workspace")
-    _same_device(a.device, w=w.data, offsets=offsets, ws=ws)
+    _same_device(a.data.device, w=w.data, offsets=offsets, ws=ws)
+    return K
 
 
 def mx4_grouped_matmul(a: Mx4, w: Mx4, offsets, out_dtype: torch.dtype = torch.bfloat16, ws=None) -> torch.Tensor:
@@ -139,15 +145,14 @@ def mx4_grouped_matmul(a: Mx4, w: Mx4, offsets, out_dtype: torch.dtype = torch.b
     the segments of offsets [E+1]; fp32 accumulation, bf16 or fp32 result.
     Rows outside every segment are not written. N must be a multiple of 8.
     ``ws``: a workspace for the error bits (``read_device_error``)."""
-    _req_product(a, w, offsets, ws)
+    K = _req_product(a, w, offsets, ws)
     if out_dtype not in _DTYPE_ID:
         raise ValueError(f"out_dtype {out_dtype}, expected bf16 or fp32")
-    rows, (E, N) = a.data.shape[0], w.data.shape[:2]
-    out = torch.empty(rows, N, dtype=out_dtype, device=a.device)
-    with _on(a.device):
-        _check(lib().moe_mx4_grouped_matmul(rows, E, N, a.K, _DTYPE_ID[out_dtype], _ptr(a.data), _ptr(a.scale),
-                                            _ptr(offsets), _ptr(w.data), _ptr(w.scale), _ptr(out), _ptr(ws),
-                                            _stream(a.device)))
+    rows, (E, N, _) = a.data.shape[0], w.data.shape
+    dev = a.data.device
+    out = torch.empty(rows, N, dtype=out_dtype, device=dev)
+    _launch(lib().moe_mx4_grouped_matmul, dev, rows, E, N, K, _DTYPE_ID[out_dtype], a.data.data_ptr(),
+            a.scale.data_ptr(), offsets.data_ptr(), w.data.data_ptr(), w.scale.data_ptr(), out.data_ptr(), _ptr(ws))
     return out
 
 
@@ -156,16 +161,16 @@ def mx4_grouped_gate_up(a: Mx4, w: Mx4, offsets, quantize: bool = False, ws=None
     rows first): h [rows, I] bf16, or with ``quantize`` that in 4 bits (the
     same bits as ``mx4_quantize`` of it). Rows outside every segment are not
     written. I must be a multiple of 32."""
-    _req_product(a, w, offsets, ws)
-    rows, (E, two_i) = a.data.shape[0], w.data.shape[:2]
+    K = _req_product(a, w, offsets, ws)
+    rows, (E, two_i, _) = a.data.shape[0], w.data.shape
     if two_i % 64 != 0:
         raise ValueError(f"w has {two_i} rows per expert, expected a multiple of 64 (twice a multiple of 32)")
     I = two_i // 2
-    h = _new((rows,), I, a.device) if quantize else torch.empty(rows, I, dtype=torch.bfloat16, device=a.device)
-    with _on(a.device):
-        _check(lib().moe_mx4_grouped_gate_up(rows, E, I, a.K, _ptr(a.data), _ptr(a.scale), _ptr(offsets),
-                                             _ptr(w.data), _ptr(w.scale), _ptr(h.data if quantize else h),
-                                             _ptr(h.scale) if quantize else None, _ptr(ws), _stream(a.device)))
+    dev = a.data.device
+    h = _new((rows,), I, dev) if quantize else torch.empty(rows, I, dtype=torch.bfloat16, device=dev)
+    data, scale = (h.data, h.scale.data_ptr()) if quantize else (h, None)
+    _launch(lib().moe_mx4_grouped_gate_up, dev, rows, E, I, K, a.data.data_ptr(), a.scale.data_ptr(),
+            offsets.data_ptr(), w.data.data_ptr(), w.scale.data_ptr(), data.data_ptr(), scale, _ptr(ws))
     return h
 
 

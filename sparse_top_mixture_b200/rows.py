@@ -16,12 +16,11 @@ their gradients as plain calls. The plan is what ``dispatch`` or
 
 from __future__ import annotations
 
-import ctypes
 from typing import Dict, Optional, Tuple
 
 import torch
 
-from . import DTYPES, Problem, _check, _on, _ptr, _req, _stream, lib
+from . import DTYPES, TORCH_DTYPE, Problem, _launch, _ptr, _req, lib
 
 
 def _plan(p: Problem, plan: Dict[str, torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -32,58 +31,52 @@ def _plan(p: Problem, plan: Dict[str, torch.Tensor]) -> Tuple[torch.Tensor, torc
 
 
 def _same_device(dev: torch.device, **tensors: Optional[torch.Tensor]) -> None:
+    index = dev.index
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
-def _y_dtype(p: Problem, y_perm) -> int:
+def _req_y(p: Problem, y_perm) -> int:
+    """The moe_dtype of y_perm [T*k, H]: fp32, or the problem's."""
     if isinstance(y_perm, torch.Tensor) and y_perm.dtype == torch.float32:
+        _req(y_perm, "y_perm", (p.T * p.k, p.H), torch.float32)
         return DTYPES["f32"]
+    _req(y_perm, "y_perm", (p.T * p.k, p.H), TORCH_DTYPE[p.dtype])
     return DTYPES[p.dtype]
 
 
-def _req_y(p: Problem, y_perm) -> int:
-    yd = _y_dtype(p, y_perm)
-    _req(y_perm, "y_perm", (p.T * p.k, p.H), torch.float32 if yd == DTYPES["f32"] else p.torch_dtype)
-    return yd
-
-
 def _permute(p: Problem, x, pair_pos, offsets):
-    out = torch.empty(p.T * p.k, p.H, dtype=p.torch_dtype, device=x.device)
-    with _on(x.device):
-        _check(lib().moe_permute_rows(ctypes.byref(p.c()), _ptr(x), _ptr(pair_pos), _ptr(offsets), _ptr(out),
-                                      _stream(x.device)))
+    dev = x.device
+    out = torch.empty(p.T * p.k, p.H, dtype=x.dtype, device=dev)
+    _launch(lib().moe_permute_rows, dev, p.c(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
 def _permute_backward(p: Problem, dx_perm, pair_pos):
-    dx = torch.empty(p.T, p.H, dtype=p.torch_dtype, device=dx_perm.device)
-    with _on(dx.device):
-        _check(lib().moe_permute_rows_backward(ctypes.byref(p.c()), _ptr(dx_perm), _ptr(pair_pos), _ptr(dx),
-                                               _stream(dx.device)))
+    dev = dx_perm.device
+    dx = torch.empty(p.T, p.H, dtype=dx_perm.dtype, device=dev)
+    _launch(lib().moe_permute_rows_backward, dev, p.c(), dx_perm.data_ptr(), pair_pos.data_ptr(), dx.data_ptr())
     return dx
 
 
 def _unpermute(p: Problem, yd: int, y_perm, pair_pos, routing_weights, shared_out):
-    out = torch.empty(p.T, p.H, dtype=p.torch_dtype, device=y_perm.device)
-    with _on(out.device):
-        _check(lib().moe_unpermute_rows(ctypes.byref(p.c()), yd, _ptr(y_perm), _ptr(pair_pos), _ptr(routing_weights),
-                                        _ptr(shared_out), _ptr(out), _stream(out.device)))
+    dev = y_perm.device
+    out = torch.empty(p.T, p.H, dtype=TORCH_DTYPE[p.dtype], device=dev)
+    _launch(lib().moe_unpermute_rows, dev, p.c(), yd, y_perm.data_ptr(), pair_pos.data_ptr(), _ptr(routing_weights),
+            _ptr(shared_out), out.data_ptr())
     return out
 
 
 def _unpermute_backward(p: Problem, yd: int, dout, y_perm, pair_pos, offsets, routing_weights, rows: bool,
                         weights: bool):
     dev = dout.device
-    dy = torch.empty(p.T * p.k, p.H, dtype=torch.float32 if yd == DTYPES["f32"] else p.torch_dtype,
+    dy = torch.empty(p.T * p.k, p.H, dtype=torch.float32 if yd == DTYPES["f32"] else TORCH_DTYPE[p.dtype],
                      device=dev) if rows else None
     dw = torch.empty(p.T, p.k, dtype=torch.float32, device=dev) if weights else None
     if rows or weights:
-        with _on(dev):
-            _check(lib().moe_unpermute_rows_backward(ctypes.byref(p.c()), yd, _ptr(dout), _ptr(y_perm),
-                                                     _ptr(pair_pos), _ptr(offsets), _ptr(routing_weights), _ptr(dy),
-                                                     _ptr(dw), _stream(dev)))
+        _launch(lib().moe_unpermute_rows_backward, dev, p.c(), yd, dout.data_ptr(), _ptr(y_perm), pair_pos.data_ptr(),
+                offsets.data_ptr(), _ptr(routing_weights), _ptr(dy), _ptr(dw))
     return dy, dw
 
 
@@ -122,10 +115,10 @@ class _UnpermuteRows(torch.autograd.Function):
 def permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]):
     """x_perm [T*k, H]: each token's row of x [T, H] copied to its k sorted
     positions. Rows past the last segment are zeros. Differentiable in x."""
-    _req(x, "x", (p.T, p.H), p.torch_dtype)
+    _req(x, "x", (p.T, p.H), TORCH_DTYPE[p.dtype])
     pair_pos, offsets = _plan(p, plan)
     _same_device(x.device, pair_pos=pair_pos, offsets=offsets)
-    if torch.is_grad_enabled() and x.requires_grad:
+    if x.requires_grad and torch.is_grad_enabled():
         return _PermuteRows.apply(x, p, pair_pos, offsets)
     return _permute(p, x, pair_pos, offsets)
 
@@ -133,7 +126,7 @@ def permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]):
 def permute_rows_backward(p: Problem, dx_perm, plan: Dict[str, torch.Tensor]):
     """dx [T, H] from dx_perm [T*k, H] (both in the problem's dtype): the sum
     of each token's k rows, in fp32, rounded once."""
-    _req(dx_perm, "dx_perm", (p.T * p.k, p.H), p.torch_dtype)
+    _req(dx_perm, "dx_perm", (p.T * p.k, p.H), TORCH_DTYPE[p.dtype])
     pair_pos, _ = _plan(p, plan)
     _same_device(dx_perm.device, pair_pos=pair_pos)
     return _permute_backward(p, dx_perm, pair_pos)
@@ -153,8 +146,8 @@ def unpermute_rows(p: Problem, y_perm, plan: Dict[str, torch.Tensor], routing_we
         _req(shared_out, "shared_out", (p.T, p.H), torch.float32)
     _same_device(y_perm.device, pair_pos=pair_pos, offsets=offsets, routing_weights=routing_weights,
                  shared_out=shared_out)
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad
-                                       for t in (y_perm, routing_weights, shared_out)):
+    if (y_perm.requires_grad or (routing_weights is not None and routing_weights.requires_grad)
+            or (shared_out is not None and shared_out.requires_grad)) and torch.is_grad_enabled():
         return _UnpermuteRows.apply(y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets)
     return _unpermute(p, yd, y_perm, pair_pos, routing_weights, shared_out)
 
@@ -164,7 +157,7 @@ def unpermute_rows_backward(p: Problem, dout, y_perm, plan: Dict[str, torch.Tens
     dout [T, H]: each row's gradient is its weight times dout (rows past the
     last segment are zeros), each weight's the product of dout and its row (0
     for a slot without a row)."""
-    _req(dout, "dout", (p.T, p.H), p.torch_dtype)
+    _req(dout, "dout", (p.T, p.H), TORCH_DTYPE[p.dtype])
     yd = _req_y(p, y_perm)
     pair_pos, offsets = _plan(p, plan)
     if routing_weights is not None:
