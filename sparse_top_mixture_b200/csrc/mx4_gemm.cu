@@ -62,34 +62,36 @@ constexpr int UNIT_BYTES = UNIT * BK / 2;
 // Scales: a row's 16-byte vector covers 512 values of K, two steps.
 constexpr int SF_ATOM_BYTES = 512;   // scale words of 128 rows for 128 values of K; a vector has four
 constexpr int MAX_STAGES = 8;
-constexpr int MAX_SF_STAGES = 4;
 constexpr int ACC_COLS = MAX_UNITS * UNIT;         // TMEM columns of one accumulator
 constexpr int SF_COL = 2 * ACC_COLS;               // two sets of scale columns follow
 constexpr int SFB_COL = 4 * 4;                     // in a set: four atoms of A, then four of B (up to 256 rows)
 constexpr int SF_SET_COLS = SFB_COL + 4 * 8;
 constexpr int TMEM_COLS = 512;
 static_assert(SF_COL + 2 * SF_SET_COLS <= TMEM_COLS, "accumulators and scales fit TMEM");
-constexpr int EPI_WARP0 = 4;
+constexpr int SF_STAGES = 4;                       // one for each scale warp
+constexpr int SF_WARP0 = 3;
+constexpr int EPI_WARP0 = SF_WARP0 + SF_STAGES;
 constexpr int GTHREADS = 32 * (EPI_WARP0 + 8);
 constexpr int STAGING_BYTES = 32 * 128;            // per epilogue warp
 
-__host__ __device__ constexpr int stage_bytes(int units) { return A_BYTES + units * UNIT_BYTES; }
-constexpr int RING_BYTES = 4 * stage_bytes(3);
-__host__ __device__ constexpr int ring_stages(int units) {
-  return RING_BYTES / stage_bytes(units) < MAX_STAGES ? RING_BYTES / stage_bytes(units) : MAX_STAGES;
+// A CTA of a pair holds its own rows of A and half of B.
+__host__ __device__ constexpr int stage_bytes(int units, bool pair) {
+  return A_BYTES + units * UNIT_BYTES / (pair ? 2 : 1);
+}
+constexpr int RING_BYTES = 4 * stage_bytes(3, false);
+__host__ __device__ constexpr int ring_stages(int units, bool pair) {
+  return RING_BYTES / stage_bytes(units, pair) < MAX_STAGES ? RING_BYTES / stage_bytes(units, pair) : MAX_STAGES;
 }
 __host__ __device__ constexpr int sfb_blocks(int units) { return (units * UNIT + 127) / 128; }
 __host__ __device__ constexpr int sf_stage_bytes(int units) { return 4 * (1 + sfb_blocks(units)) * SF_ATOM_BYTES; }
-constexpr int SF_RING_BYTES = 3 * sf_stage_bytes(3);
-__host__ __device__ constexpr int sf_stages(int units) { return SF_RING_BYTES / sf_stage_bytes(units); }
-static_assert(sf_stages(1) <= MAX_SF_STAGES && sf_stages(2) <= MAX_SF_STAGES, "scale barriers");
+constexpr int SF_RING_BYTES = SF_STAGES * sf_stage_bytes(3);
 
 enum { OUT_BF16 = 0, OUT_F32 = 1, SWIGLU_BF16 = 2, SWIGLU_MX4 = 3 };
 constexpr bool is_swiglu(int mode) { return mode >= SWIGLU_BF16; }
 
 struct Maps {
   CUtensorMap a_box, a_tile;  // A in boxes of 32 rows, and of 128
-  CUtensorMap b[MAX_UNITS];   // W in boxes of 1..3 units
+  CUtensorMap b[MAX_UNITS];   // W in boxes of 1..3 units; a pair's first: of half a tile's rows
   CUtensorMap out;            // out in a warp's staged boxes
 };
 
@@ -114,11 +116,14 @@ struct Args {
 struct __align__(8) Ctl {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
-  uint64_t sfull[MAX_SF_STAGES];
-  uint64_t sempty[MAX_SF_STAGES];
+  uint64_t sfull[SF_STAGES];
+  uint64_t sempty[SF_STAGES];
+  uint64_t cfull[2];   // a set of scale columns is filled, and free again
+  uint64_t cempty[2];
   uint64_t tfull[2];
   uint64_t tempty[2];
-  uint64_t drain;
+  uint64_t drain;   // every MMA is done, and every copy of scales
+  uint64_t cdrain;
   uint32_t tmem_base;
   int abort;
   int units;
@@ -134,8 +139,8 @@ static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 // major, N>>3 in bits 17-22, scales ue8m0 (bit 23), M>>4 in 24-28; which half
 // of the scale words (0, or 2 for the second 64 values) in bits 4-5 for B and
 // 29-30 for A.
-__device__ __forceinline__ uint32_t make_idesc_mxf4(int N, uint32_t half) {
-  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(BM >> 4) << 24) |
+__device__ __forceinline__ uint32_t make_idesc_mxf4(int M, int N, uint32_t half) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (1u << 23) | ((uint32_t)(M >> 4) << 24) |
          (half << 4) | (half << 29);
 }
 
@@ -145,18 +150,49 @@ __device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
   return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
 }
 
+// Of a pair, both CTAs copy from their own shared memory to their own TMEM.
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  if constexpr (PAIR)
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+  else
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
-      : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on `bar` once the work that this thread has issued so far is done;
+// commit: of a pair, in both CTAs.
+template <bool PAIR>
+__device__ __forceinline__ void commit_here(uint64_t* bar) {
+  if constexpr (PAIR)
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+  else
+    umma_commit(bar);
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  if constexpr (PAIR) umma2_commit_mc(bar, 0x3);
+  else umma_commit(bar);
 }
 
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -214,15 +250,17 @@ struct Tile {
   int e, row0, row_end, unit0;
 };
 
-// The tile's place; e is the expert of an earlier tile of the same CTA (row
+// The tile's place (of a pair's, this CTA's 128 rows, which may lie past the
+// segment); e is the expert of an earlier tile of the same CTA (row
 // tiles come in rising order).
-__device__ __forceinline__ Tile decode(const Ctl* ctl, int units, int n_tiles, int tile, int e) {
+template <bool PAIR>
+__device__ __forceinline__ Tile decode(const Ctl* ctl, int units, int n_tiles, int tile, int e, int rank) {
   Tile t;
   const int mt = tile / n_tiles;
   t.unit0 = (tile - mt * n_tiles) * units;
   while (ctl->pre[e + 1] <= mt) ++e;
   t.e = e;
-  t.row0 = ctl->off[e] + (mt - ctl->pre[e]) * BM;
+  t.row0 = ctl->off[e] + (mt - ctl->pre[e]) * (PAIR ? 2 * BM : BM) + rank * BM;
   t.row_end = ctl->off[e + 1];
   return t;
 }
@@ -287,8 +325,8 @@ __device__ __forceinline__ void box_free(int lane) {
   __syncwarp();
 }
 
-template <int MODE>
-__global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+template <int MODE, bool PAIR>
+__device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sf_base = base + RING_BYTES;
@@ -296,39 +334,51 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
   Ctl* ctl = reinterpret_cast<Ctl*>(staging + 8 * STAGING_BYTES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const int rank = PAIR ? (int)cluster_ctarank() : 0;
+  const bool leader = rank == 0;
+  // a worker is a CTA, or a pair
+  const int worker = PAIR ? blockIdx.x >> 1 : blockIdx.x, workers = PAIR ? gridDim.x >> 1 : gridDim.x;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(&ctl->full[s], 1);
       mbar_init(&ctl->empty[s], 1);
     }
-    for (int s = 0; s < MAX_SF_STAGES; ++s) {
-      mbar_init(&ctl->sfull[s], 2);  // the two scale warps
+    for (int s = 0; s < SF_STAGES; ++s) {
+      mbar_init(&ctl->sfull[s], PAIR ? 2 : 1);  // a scale warp, of a pair's both CTAs
       mbar_init(&ctl->sempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
+      mbar_init(&ctl->cfull[a], 1);
+      mbar_init(&ctl->cempty[a], 1);
       mbar_init(&ctl->tfull[a], 1);
-      mbar_init(&ctl->tempty[a], 128);
+      mbar_init(&ctl->tempty[a], PAIR ? 8 : 4);  // the accumulator's epilogue warps
     }
     mbar_init(&ctl->drain, 1);
+    mbar_init(&ctl->cdrain, 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
-  if (warp == 2) {
-    warp_build_tile_table(args.offsets, args.E, 0, BM, ctl->off, ctl->pre, args.rows_total, args.err);
+  if (warp == SF_WARP0) {
+    warp_build_tile_table(args.offsets, args.E, 0, PAIR ? 2 * BM : BM, ctl->off, ctl->pre, args.rows_total, args.err);
     __syncwarp();
     if (lane == 0) {
       const int row_tiles = ctl->pre[args.E];
-      ctl->units = choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units,
-                                (int)gridDim.x);
+      ctl->units = PAIR ? MAX_UNITS
+                        : choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units,
+                                       workers);
     }
   }
-  if (warp == 1) tmem_alloc(&ctl->tmem_base, TMEM_COLS);
+  if (warp == 1) {
+    if constexpr (PAIR) tmem_alloc2(&ctl->tmem_base, TMEM_COLS);
+    else tmem_alloc(&ctl->tmem_base, TMEM_COLS);
+  }
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // the peer's barriers exist before any remote arrive
   tc_fence_after();
   const uint32_t tmem_base = ctl->tmem_base;
-  const int units = ctl->units;
+  const int units = PAIR ? MAX_UNITS : ctl->units;
   const int n_tiles = (args.n_units + units - 1) / units;
   const int total = ctl->pre[args.E] * n_tiles;
   const int blocks = sfb_blocks(units);
@@ -336,18 +386,24 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
   if (warp == 0) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
-      const int stages = ring_stages(units), sbytes = stage_bytes(units);
+      const int stages = ring_stages(units, PAIR), sbytes = stage_bytes(units, PAIR);
       int stage = 0, e = 0;
       uint32_t phase = 0, issued = 0, last_parity = 0;
       bool ok = true;
-      const CUtensorMap* tmB = &maps.b[units - 1];
+      const CUtensorMap* tmB = &maps.b[PAIR ? 0 : units - 1];
       bool seen = false;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const Tile t = decode(ctl, units, n_tiles, tile, e);
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
         e = t.e;
-        const int boxes = (t.row_end - t.row0 + A_BOX_ROWS - 1) / A_BOX_ROWS;
-        const bool whole = boxes >= BM / A_BOX_ROWS;
-        const uint32_t bytes = (uint32_t)((whole ? A_BYTES : boxes * (A_BYTES * A_BOX_ROWS / BM)) + units * UNIT_BYTES);
+        // boxes of A that the rows from row0 on fill, and their bytes
+        auto boxes_from = [&](int row0) {
+          return max(0, min(BM / A_BOX_ROWS, (t.row_end - row0 + A_BOX_ROWS - 1) / A_BOX_ROWS));
+        };
+        const int boxes = boxes_from(t.row0);
+        const bool whole = boxes == BM / A_BOX_ROWS;
+        // A pair's bytes are all counted by the leader's barrier.
+        const uint32_t bytes = (uint32_t)((boxes + (PAIR ? boxes_from(t.row0 + BM) : 0)) * (A_BYTES * A_BOX_ROWS / BM) +
+                                          units * UNIT_BYTES);
         const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT);
         for (int kt = 0; kt < args.k_steps; ++kt) {
           if (!seen && !mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
@@ -359,14 +415,28 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
           seen = mbar_test(&ctl->empty[next], next_phase ^ 1u);
           uint8_t* sa = base + stage * sbytes;
           const int kb = kt * (BK / 2);
-          mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-          tma_load_4d(sa + A_BYTES, tmB, &ctl->full[stage], kb, n0, 0, t.e);
-          if (whole) {
-            tma_load_2d(sa, &maps.a_tile, &ctl->full[stage], kb, t.row0);
+          if constexpr (PAIR) {
+            const uint32_t full = mapa_shared(smem_u32(&ctl->full[stage]), 0);
+            if (leader) mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+            // gate_up: the leader loads the gate rows, its peer the up rows
+            tma2_load_4d(sa + A_BYTES, tmB, full, kb, is_swiglu(MODE) ? n0 : n0 + rank * (MAX_UNITS * UNIT / 2),
+                         is_swiglu(MODE) ? rank : 0, t.e);
+            if (whole) {
+              tma2_load_2d(sa, &maps.a_tile, full, kb, t.row0);
+            } else {
+              for (int i = 0; i < boxes; ++i)
+                tma2_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, full, kb, t.row0 + A_BOX_ROWS * i);
+            }
           } else {
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, &ctl->full[stage], kb,
-                          t.row0 + A_BOX_ROWS * i);
+            mbar_arrive_expect_tx(&ctl->full[stage], bytes);
+            tma_load_4d(sa + A_BYTES, tmB, &ctl->full[stage], kb, n0, 0, t.e);
+            if (whole) {
+              tma_load_2d(sa, &maps.a_tile, &ctl->full[stage], kb, t.row0);
+            } else {
+              for (int i = 0; i < boxes; ++i)
+                tma_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, &ctl->full[stage], kb,
+                            t.row0 + A_BOX_ROWS * i);
+            }
           }
           issued |= 1u << stage;
           last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
@@ -374,57 +444,31 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
           phase = next_phase;
         }
       }
-      // Every copy has landed before the CTA may exit.
+      // Every copy has landed before the CTA may exit (a pair's leader counts
+      // both CTAs' bytes, and the CTAs exit together).
       for (int s = 0; s < stages; ++s)
-        if ((issued >> s) & 1u) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
+        if (leader && ((issued >> s) & 1u)) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    if (elect_one()) {
-      const int stages = ring_stages(units), sbytes = stage_bytes(units);
-      const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
-      const uint32_t smem_base = smem_u32(base), sf_smem = smem_u32(sf_base);
-      const uint32_t idesc0 = make_idesc_mxf4(units * UNIT, 0), idesc2 = make_idesc_mxf4(units * UNIT, 2);
+    if (leader && elect_one()) {
+      const int stages = ring_stages(units, PAIR), sbytes = stage_bytes(units, PAIR);
+      const uint32_t smem_base = smem_u32(base);
+      constexpr int M = PAIR ? 2 * BM : BM;
+      const uint32_t idesc0 = make_idesc_mxf4(M, units * UNIT, 0), idesc2 = make_idesc_mxf4(M, units * UNIT, 2);
       const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
-      int stage = 0, sf_stage = 0, acc = 0, set = 0;
-      uint32_t phase = 0, sf_phase = 0, acc_phase = 0;
-      bool ok = true, seen = false, sf_seen = false;
-      for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      int stage = 0, acc = 0, set = 0;
+      uint32_t phase = 0, set_phase = 0, acc_phase = 0;
+      bool ok = true, seen = false, set_seen = false;
+      for (int tile = worker; ok && tile < total; tile += workers) {
         if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-        uint32_t sfa = 0, sfb = 0;
         for (int kt = 0; kt < args.k_steps; ++kt) {
-          if ((kt & 1) == 0) {
-            // The scales of two steps to TMEM. The tensor core takes copies and
-            // MMAs in the order of their issue; the other set is still in use.
-            if (!sf_seen && !mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 8)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            sfa = tmem_base + SF_COL + set * SF_SET_COLS;
-            sfb = sfa + SFB_COL;
-            const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes), db = da + 4 * (SF_ATOM_BYTES / 16);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) copy_scales(sfa + 4 * i, da + i * (SF_ATOM_BYTES / 16));
-            if (blocks == 1) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) copy_scales(sfb + 8 * i, db + i * (SF_ATOM_BYTES / 16));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i) copy_scales(sfb + 4 * i, db + i * (SF_ATOM_BYTES / 16));
-            }
-            umma_commit(&ctl->sempty[sf_stage]);
-            set ^= 1;
-            if (++sf_stage == sf_count) {
-              sf_stage = 0;
-              sf_phase ^= 1u;
-            }
-          } else {
-            sfa += 2 * 4;
-            sfb += 2 * 8;
+          if ((kt & 1) == 0 && !set_seen && !mbar_wait(&ctl->cfull[set], set_phase, &ctl->abort, args.err, 8)) {
+            ok = false;
+            break;
           }
           if (!seen && !mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
             ok = false;
@@ -434,119 +478,168 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
           const int next = stage + 1 == stages ? 0 : stage + 1;
           const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
           seen = mbar_test(&ctl->full[next], next_phase);
-          sf_seen = mbar_test(&ctl->sfull[sf_stage], sf_phase);
           const uint32_t sa = smem_base + stage * sbytes;
+          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS + (kt & 1) * 8;
+          const uint32_t sfb = tmem_base + SF_COL + set * SF_SET_COLS + SFB_COL + (kt & 1) * 16;
           const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
-          const int left = kt + 1 < args.k_steps ? BK : k_tail;
-          umma_mxf4(d_tmem, adesc, bdesc, idesc0, sfa, sfb, kt > 0 ? 1u : 0u);
-          if (left > 64) umma_mxf4(d_tmem, adesc + 2, bdesc + 2, idesc2, sfa, sfb, 1u);
-          if (left > 128) umma_mxf4(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 8, 1u);
-          if (left > 192) umma_mxf4(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 8, 1u);
-          umma_commit(&ctl->empty[stage]);
+          const bool last = kt + 1 == args.k_steps;
+          const int left = last ? k_tail : BK;
+          umma_mxf4<PAIR>(d_tmem, adesc, bdesc, idesc0, sfa, sfb, kt > 0 ? 1u : 0u);
+          if (left > 64) umma_mxf4<PAIR>(d_tmem, adesc + 2, bdesc + 2, idesc2, sfa, sfb, 1u);
+          if (left > 128) umma_mxf4<PAIR>(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 8, 1u);
+          if (left > 192) umma_mxf4<PAIR>(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 8, 1u);
+          commit<PAIR>(&ctl->empty[stage]);
           stage = next;
           phase = next_phase;
+          if ((kt & 1) || last) {
+            commit_here<PAIR>(&ctl->cempty[set]);
+            set ^= 1;
+            if (set == 0) set_phase ^= 1u;
+            set_seen = mbar_test(&ctl->cfull[set], set_phase);
+          }
         }
         if (!ok) break;
-        umma_commit(&ctl->tfull[acc]);
+        commit<PAIR>(&ctl->tfull[acc]);
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      umma_commit(&ctl->drain);
+      commit<PAIR>(&ctl->drain);
       mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     }
+    if (PAIR && !leader) mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     __syncwarp();
-  } else if (warp < EPI_WARP0) {
-    // ---------------- scale producers (warp 2: A, warp 3: B) ----------------
-    // Two vectors are loaded ahead of the one that is stored, across tiles.
-    constexpr int kSlots = MAX_UNITS * UNIT / 32;  // rows of a lane; A has 4
-    const bool is_b = warp == 3;
-    const int sf_count = sf_stages(units), sf_bytes = sf_stage_bytes(units);
-    const int n_vec = (args.k_steps + 1) / 2;
-    int tile = blockIdx.x, kv = n_vec, e = 0;  // the next vector to load; kv == n_vec: the tile is not set up yet
-    const uint4* src[kSlots];  // this lane's rows' scales, nullptr for a row that the tile lacks
-    auto load = [&](uint4 (&v)[kSlots]) -> int {
-      if (tile >= total) return -1;
-      if (kv == n_vec) {
-        kv = 0;
-        const Tile t = decode(ctl, units, n_tiles, tile, e);
-        e = t.e;
-        if (is_b) {
-          const uint8_t* w = args.b_scale + (int64_t)e * args.b_rows * args.pitch;
+  } else if (warp == 2) {
+    // ---------------- scales from shared memory to TMEM ----------------
+    // A thread of its own: the twelve copies of a vector would take the MMA's
+    // a third of its time.
+    if (leader && elect_one()) {
+      const int sf_bytes = sf_stage_bytes(units), n_vec = (args.k_steps + 1) / 2;
+      const uint32_t sf_smem = smem_u32(sf_base);
+      int sf_stage = 0, set = 0;
+      uint32_t sf_phase = 0, set_phase = 0;
+      bool ok = true;
+      for (int tile = worker; ok && tile < total; tile += workers) {
+        for (int kv = 0; kv < n_vec; ++kv) {
+          ok = mbar_wait(&ctl->cempty[set], set_phase ^ 1u, &ctl->abort, args.err, 9) &&
+               mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 10);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS, sfb = sfa + SFB_COL;
+          const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes), db = da + 4 * (SF_ATOM_BYTES / 16);
 #pragma unroll
-          for (int c = 0; c < kSlots; ++c) {
-            // gate_up: the tile's gate rows, 32 a unit, then its up rows
-            const int up = is_swiglu(MODE) && c >= units ? 1 : 0;
-            const int n = is_swiglu(MODE) ? (t.unit0 + c - up * units) * 32 + lane : t.unit0 * UNIT + 32 * c + lane;
-            const int64_t row = (int64_t)up * args.N + n;
-            src[c] = c < 2 * units && n < args.N ? reinterpret_cast<const uint4*>(w + row * args.pitch) : nullptr;
+          for (int i = 0; i < 4; ++i) copy_scales<PAIR>(sfa + 4 * i, da + i * (SF_ATOM_BYTES / 16));
+          if (blocks == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) copy_scales<PAIR>(sfb + 8 * i, db + i * (SF_ATOM_BYTES / 16));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) copy_scales<PAIR>(sfb + 4 * i, db + i * (SF_ATOM_BYTES / 16));
           }
-        } else {
-#pragma unroll
-          for (int c = 0; c < kSlots; ++c) {
-            const int row = t.row0 + 32 * c + lane;
-            src[c] = c < 4 && row < t.row_end
-                         ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch)
-                         : nullptr;
+          commit_here<PAIR>(&ctl->cfull[set]);
+          commit<PAIR>(&ctl->sempty[sf_stage]);
+          set ^= 1;
+          if (set == 0) set_phase ^= 1u;
+          if (++sf_stage == SF_STAGES) {
+            sf_stage = 0;
+            sf_phase ^= 1u;
           }
         }
       }
-#pragma unroll
-      for (int c = 0; c < kSlots; ++c) v[c] = src[c] ? __ldg(src[c] + kv) : make_uint4(0, 0, 0, 0);
-      const int at = kv;
-      if (++kv == n_vec) tile += gridDim.x;
-      return at;
-    };
-    int stage = 0;
+      commit<PAIR>(&ctl->cdrain);
+      mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
+    }
+    if (PAIR && !leader) mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
+    __syncwarp();
+  } else if (warp < EPI_WARP0) {
+    // ---------------- scale producers ----------------
+    // The warps take the vectors of the CTA's tiles in turn, each into a stage of
+    // its own, so that the loads of several are in flight. (One warp that loads ahead of what it stores
+    // gains nothing: its fence waits for all its loads.)
+    constexpr int kA = BM / 32, kB = MAX_UNITS * UNIT / 32;  // rows of a lane
+    const int n_vec = (args.k_steps + 1) / 2, stage = warp - SF_WARP0;
+    uint8_t* const stage_base = sf_base + stage * sf_stage_bytes(units) + lane * 16;
+    int tile = worker, kv = stage, e = 0;
     uint32_t phase = 0;
-    auto publish = [&](const uint4 (&v)[kSlots], int at) -> bool {
-      if (!warp_wait(&ctl->sempty[stage], phase ^ 1u, &ctl->abort, args.err, 5)) return false;
-      uint8_t* dst = sf_base + stage * sf_bytes + (is_b ? 4 * SF_ATOM_BYTES : 0) + lane * 16;
+    const uint4 *src_a[kA], *src_b[kB];  // this lane's rows' scales, nullptr for a row that the tile lacks
+    for (bool set_up = true;;) {
+      for (; kv >= n_vec; kv -= n_vec) {
+        tile += workers;
+        set_up = true;
+      }
+      if (tile >= total) break;
+      if (set_up) {
+        set_up = false;
+        const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
+        e = t.e;
+#pragma unroll
+        for (int c = 0; c < kA; ++c) {
+          const int row = t.row0 + 32 * c + lane;
+          src_a[c] = row < t.row_end ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch) : nullptr;
+        }
+        const uint8_t* w = args.b_scale + (int64_t)e * args.b_rows * args.pitch;
+#pragma unroll
+        for (int c = 0; c < kB; ++c) {
+          // gate_up: the tile's gate rows, 32 a unit, then its up rows
+          const int up = is_swiglu(MODE) && c >= units ? 1 : 0;
+          const int n = is_swiglu(MODE) ? (t.unit0 + c - up * units) * 32 + lane : t.unit0 * UNIT + 32 * c + lane;
+          const int64_t row = (int64_t)up * args.N + n;
+          src_b[c] = c < 2 * units && n < args.N ? reinterpret_cast<const uint4*>(w + row * args.pitch) : nullptr;
+        }
+      }
+      uint4 va[kA], vb[kB];
+#pragma unroll
+      for (int c = 0; c < kA; ++c) va[c] = src_a[c] ? __ldg(src_a[c] + kv) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int c = 0; c < kB; ++c) vb[c] = src_b[c] ? __ldg(src_b[c] + kv) : make_uint4(0, 0, 0, 0);
+      if (!warp_wait(&ctl->sempty[stage], phase ^ 1u, &ctl->abort, args.err, 5)) break;
 #pragma unroll
       for (int atom = 0; atom < 4; ++atom) {
         // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
-        const int valid = args.K / mx4::kBlock - at * 16 - atom * 4;
+        const int valid = args.K / mx4::kBlock - kv * 16 - atom * 4;
         const uint32_t mask = valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-        auto word = [&](int c) {
-          return mask & (atom == 0 ? v[c].x : atom == 1 ? v[c].y : atom == 2 ? v[c].z : v[c].w);
-        };
-        const uint4 lo = make_uint4(word(0), word(1), word(2), word(3));
-        if (is_b && blocks == 2) {
-          *reinterpret_cast<uint4*>(dst + 2 * atom * SF_ATOM_BYTES) = lo;
-          *reinterpret_cast<uint4*>(dst + (2 * atom + 1) * SF_ATOM_BYTES) = make_uint4(word(4), word(5), 0u, 0u);
+        auto word = [&](const uint4& v) { return mask & (atom == 0 ? v.x : atom == 1 ? v.y : atom == 2 ? v.z : v.w); };
+        *reinterpret_cast<uint4*>(stage_base + atom * SF_ATOM_BYTES) = make_uint4(word(va[0]), word(va[1]), word(va[2]), word(va[3]));
+        const uint4 lo = make_uint4(word(vb[0]), word(vb[1]), word(vb[2]), word(vb[3]));
+        uint8_t* dst_b = stage_base + 4 * SF_ATOM_BYTES;
+        if (blocks == 2) {
+          *reinterpret_cast<uint4*>(dst_b + 2 * atom * SF_ATOM_BYTES) = lo;
+          *reinterpret_cast<uint4*>(dst_b + (2 * atom + 1) * SF_ATOM_BYTES) = make_uint4(word(vb[4]), word(vb[5]), 0u, 0u);
         } else {
-          *reinterpret_cast<uint4*>(dst + atom * SF_ATOM_BYTES) = lo;
+          *reinterpret_cast<uint4*>(dst_b + atom * SF_ATOM_BYTES) = lo;
         }
       }
       fence_to_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->sfull[stage]);
-      if (++stage == sf_count) {
-        stage = 0;
-        phase ^= 1u;
+      if (lane == 0) {
+        // To a pair's leader without a release at cluster scope: the fences have
+        // put the stores where the leader's copy of this CTA's memory reads, and
+        // such a release would wait about 1000 clocks for loads in flight.
+        if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->sfull[stage]), 0));
+        else mbar_arrive(&ctl->sfull[stage]);
       }
-      return true;
-    };
-    uint4 v0[kSlots], v1[kSlots];
-    int at0 = load(v0), at1 = load(v1);
-    while (at0 >= 0) {
-      if (!publish(v0, at0)) break;
-      at0 = load(v0);
-      if (at1 < 0) break;
-      if (!publish(v1, at1)) break;
-      at1 = load(v1);
+      kv += SF_STAGES;
+      phase ^= 1u;
     }
     __syncwarp();
   } else {
-    // ---------------- epilogue: warps 4..7 take the first accumulator's tiles, 8..11 the second's ----------------
+    // ---------------- epilogue: four warps take the first accumulator's tiles, four the second's ----------------
     const int quarter = warp & 3;  // TMEM lanes this warp may access
     const int acc = (warp - EPI_WARP0) >> 2;
     const uint32_t tbase = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+    auto release = [&] {  // the warp has read the accumulator
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->tempty[acc]), 0));
+        else mbar_arrive(&ctl->tempty[acc]);
+      }
+    };
     uint8_t* stg = staging + (warp - EPI_WARP0) * STAGING_BYTES;
     uint32_t acc_phase = 0;
     int e = 0;
     [[maybe_unused]] int other = 0;
-    for (int tile = blockIdx.x + acc * (int)gridDim.x; tile < total; tile += 2 * gridDim.x) {
-      const Tile t = decode(ctl, units, n_tiles, tile, e);
+    for (int tile = worker + acc * workers; tile < total; tile += 2 * workers) {
+      const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
       e = t.e;
       const int row_w0 = t.row0 + quarter * 32;
       const int nrows = t.row_end - row_w0;
@@ -563,10 +656,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
             tmem_ld32(tbase + (units + j) * 32, u);
             tmem_ld_wait_regs(g);
             tmem_ld_wait_regs(u);
-            if (j + 1 == count) {  // the tile's last read
-              tc_fence_before();
-              mbar_arrive(&ctl->tempty[acc]);
-            }
+            if (j + 1 == count) release();  // the tile's last read
             const int n0 = (t.unit0 + j) * 32;  // N is a multiple of 32: the block lies inside
             uint32_t h[16];
 #pragma unroll
@@ -635,10 +725,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
               tmem_ld32(tbase + c0, v);
               tmem_ld_wait_regs(v);
             }
-            if (c0 + kCols >= count) {  // the tile's last read
-              tc_fence_before();
-              mbar_arrive(&ctl->tempty[acc]);
-            }
+            if (c0 + kCols >= count) release();  // the tile's last read
             box_free<0>(lane);
 #pragma unroll
             for (int c = 0; c < 8; ++c)
@@ -650,8 +737,7 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
           }
         }
       } else {
-        tc_fence_before();
-        mbar_arrive(&ctl->tempty[acc]);
+        release();
       }
     }
     if constexpr (MODE != SWIGLU_MX4) box_free<0>(lane);
@@ -659,20 +745,34 @@ __global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_cons
 
   tc_fence_before();
   __syncthreads();
+  if constexpr (PAIR) cluster_sync_all();  // no remote arrive or pair MMA still targets either CTA
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    if constexpr (PAIR) tmem_dealloc2(tmem_base, TMEM_COLS);
+    else tmem_dealloc(tmem_base, TMEM_COLS);
   }
 }
 
 template <int MODE>
+__global__ void __launch_bounds__(GTHREADS, 1) mx4_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+  mx4_gemm<MODE, false>(maps, args);
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(GTHREADS, 1)
+    mx4_pair_gemm_kernel(const __grid_constant__ Maps maps, const Args args) {
+  mx4_gemm<MODE, true>(maps, args);
+}
+
+template <int MODE, bool PAIR>
 cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_data, const void* a_scale,
                    const int32_t* offsets, const void* w_data, const void* w_scale, void* out, void* out_scale,
                    int32_t* err, cudaStream_t s) {
   static std::once_flag once[kSmemAttrDevices];  // one set per kernel instance
   static cudaError_t attr[kSmemAttrDevices];
-  const void* kernel = reinterpret_cast<const void*>(mx4_gemm_kernel<MODE>);
+  void (*const kernel_fn)(Maps, Args) = PAIR ? mx4_pair_gemm_kernel<MODE> : mx4_gemm_kernel<MODE>;
+  const void* kernel = reinterpret_cast<const void*>(kernel_fn);
   const cudaError_t e = set_max_dynamic_smem_once(kernel, (int)kSmemBytes, once, attr);
   if (e != cudaSuccess) return e;
   if (!get_encode()) return cudaErrorNotSupported;
@@ -685,12 +785,13 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
                          CU_TENSOR_MAP_SWIZZLE_128B, a_data, 2, dims, strides, box))
       return cudaErrorInvalidValue;
   }
-  for (int u = 1; u <= MAX_UNITS; ++u) {
+  for (int u = 1; u <= (PAIR ? 1 : MAX_UNITS); ++u) {
     // W [E][halves][N][K/2]: gate_up's two halves, or one
     const uint64_t halves = is_swiglu(MODE) ? 2 : 1;
     const uint64_t dims[4] = {(uint64_t)K / 2, (uint64_t)N, halves, (uint64_t)E};
     const uint64_t strides[3] = {(uint64_t)K / 2, (uint64_t)N * K / 2, halves * (uint64_t)N * K / 2};
-    const uint32_t box[4] = {BK / 2, (uint32_t)(u * UNIT / halves), (uint32_t)halves, 1};
+    const uint32_t box[4] = {BK / 2, PAIR ? MAX_UNITS * UNIT / 2u : (uint32_t)(u * UNIT / halves),
+                             PAIR ? 1u : (uint32_t)halves, 1};
     if (!make_tensor_map(&maps.b[u - 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
   }
   if (MODE != SWIGLU_MX4) {
@@ -719,10 +820,23 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   a.out_scale = static_cast<uint8_t*>(out_scale);
   a.out_pitch = (int32_t)mx4::scale_pitch(N);
   a.err = err;
-  const int64_t most = (rows / BM + std::min<int64_t>(rows, E)) * a.n_units;  // tiles of one unit
-  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms(), most));
-  mx4_gemm_kernel<MODE><<<grid, GTHREADS, kSmemBytes, s>>>(maps, a);
+  // tiles of one unit, or of a pair
+  const int64_t most = PAIR ? (rows / (2 * BM) + std::min<int64_t>(rows, E)) * ceil_div(a.n_units, MAX_UNITS)
+                            : (rows / BM + std::min<int64_t>(rows, E)) * a.n_units;
+  const int workers = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / (PAIR ? 2 : 1), most));
+  kernel_fn<<<workers * (PAIR ? 2 : 1), GTHREADS, kSmemBytes, s>>>(maps, a);
   return cudaGetLastError();
+}
+
+bool use_pairs(int64_t rows, int64_t E, int64_t n_units) { return rows >= 512 * E && n_units >= MAX_UNITS; }
+
+template <int MODE>
+cudaError_t launch_product(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_data, const void* a_scale,
+                           const int32_t* offsets, const void* w_data, const void* w_scale, void* out, void* out_scale,
+                           int32_t* err, cudaStream_t s) {
+  const bool pairs = use_pairs(rows, E, ceil_div(N, is_swiglu(MODE) ? UNIT / 2 : UNIT));
+  return pairs ? launch<MODE, true>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, out_scale, err, s)
+               : launch<MODE, false>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, out_scale, err, s);
 }
 
 bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -759,8 +873,8 @@ MOE_API moe_status moe_mx4_grouped_matmul(int64_t rows, int64_t E, int64_t N, in
   int32_t* err = static_cast<int32_t*>(ws);
   const cudaError_t e =
       out_dtype == MOE_DTYPE_F32
-          ? launch<OUT_F32>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s)
-          : launch<OUT_BF16>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s);
+          ? launch_product<OUT_F32>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s)
+          : launch_product<OUT_BF16>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, nullptr, err, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -778,7 +892,7 @@ MOE_API moe_status moe_mx4_grouped_gate_up(int64_t rows, int64_t E, int64_t I, i
   int32_t* err = static_cast<int32_t*>(ws);
   const cudaError_t e =
       h_scale == nullptr
-          ? launch<SWIGLU_BF16>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, nullptr, err, s)
-          : launch<SWIGLU_MX4>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, h_scale, err, s);
+          ? launch_product<SWIGLU_BF16>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, nullptr, err, s)
+          : launch_product<SWIGLU_MX4>(rows, E, I, H, a_data, a_scale, offsets, w_data, w_scale, h, h_scale, err, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
