@@ -25,13 +25,30 @@ constexpr int QTHREADS = 256;
 constexpr int kPasses = 4;
 constexpr int kChunk = kPasses * 256;  // values per warp
 
+// Eight values as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* f) {
+struct Raw8 {
+  uint4 v[sizeof(T) / 2];
+};
+
+// The values at p, or zeros: selected, not branched round, so that the loads of
+// a thread go out together.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load8(const T* p, bool inside) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+    r.v[i] = inside ? __ldcs(reinterpret_cast<const uint4*>(p) + i) : make_uint4(0u, 0u, 0u, 0u);
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void values8(const Raw8<T>& r, float* f) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    unpack16(r.v[0], f, static_cast<float*>(nullptr));
+    unpack16(r.v[1], f + 4, static_cast<float*>(nullptr));
   } else {
-    unpack16_bf16(__ldcs(reinterpret_cast<const uint4*>(p)), f);
+    unpack16_bf16(r.v[0], f);
   }
 }
 
@@ -50,30 +67,27 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const T* __restrict_
   for (int64_t it = warp0; it < rows * chunks; it += warps) {
     const int64_t row = it / chunks;
     const int c0 = (int)(it - row * chunks) * kChunk;
-    float f[kPasses][8];
+    Raw8<T> raw[kPasses];
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
       const int col = c0 + u * 256 + lane * 8;
-      if (col < K) {
-        load8(x + row * K + col, f[u]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[u][i] = 0.f;
-      }
+      raw[u] = load8(x + row * K + col, col < K);
     }
     uint32_t code[kPasses], b[kPasses];
 #pragma unroll
     for (int u = 0; u < kPasses; ++u) {
+      float f[8];
+      values8(raw[u], f);
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[u][i]) & 0x7fffffffu);
+      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
       b[u] = scale_byte(m);
       const float inv = inverse_scale(b[u]);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[u][i] *= inv;
-      code[u] = b[u] == kScaleNaN ? 0u : pack8(f[u]);
+      for (int i = 0; i < 8; ++i) f[i] *= inv;
+      code[u] = b[u] == kScaleNaN ? 0u : pack8(f);
     }
     const int pad0 = K / kBlock;  // the row's last chunk also writes the padding
     auto store = [&](int64_t r) {
@@ -146,9 +160,14 @@ __global__ void __launch_bounds__(QTHREADS) dequantize_kernel(const uint32_t* __
 
 bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-unsigned warp_grid(int64_t items) {
-  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, QTHREADS / 32), 148 * 8));
+// Blocks for `items` warps' work, at most `most`.
+unsigned warp_grid(int64_t items, int64_t most = 148 * 8) {
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(ceil_div(items, QTHREADS / 32), most));
 }
+
+// Dequantisation, which mostly stores, runs with blocks that are replaced as
+// they end (45056 x 2048 to bf16: 39 us, with resident blocks 46).
+constexpr int64_t kManyBlocks = 148 * 8 * 64;
 
 moe_status check_rows(int64_t rows, int64_t K, int32_t dtype) {
   if (rows < 0 || K <= 0 || K % kBlock != 0 || K >= (int64_t(1) << 31) || rows >= (int64_t(1) << 31))
@@ -194,10 +213,10 @@ MOE_API moe_status moe_mx4_dequantize(int64_t rows, int64_t K, int32_t dtype, co
   const uint32_t* d = static_cast<const uint32_t*>(data);
   const uint8_t* sc = static_cast<const uint8_t*>(scale);
   if (dtype == MOE_DTYPE_F32)
-    dequantize_kernel<float><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(d, sc, rows, (int)K, pitch, chunks,
+    dequantize_kernel<float><<<warp_grid(rows * chunks, kManyBlocks), QTHREADS, 0, s>>>(d, sc, rows, (int)K, pitch, chunks,
                                                                            static_cast<float*>(out));
   else
-    dequantize_kernel<__nv_bfloat16><<<warp_grid(rows * chunks), QTHREADS, 0, s>>>(
+    dequantize_kernel<__nv_bfloat16><<<warp_grid(rows * chunks, kManyBlocks), QTHREADS, 0, s>>>(
         d, sc, rows, (int)K, pitch, chunks, static_cast<__nv_bfloat16*>(out));
   return status(cudaGetLastError());
 }

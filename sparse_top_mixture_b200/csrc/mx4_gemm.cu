@@ -7,33 +7,37 @@
 //             bf16, or rounded to bf16 and then quantised to 4 bits
 //
 // The MMA multiplies 64 values of K at a time by their two scale bytes per row
-// and accumulates in fp32; nothing is dequantised. Large batches are bound by
-// getting operands to the tensor cores (at 4 bits a 128 x 192 x 256 step needs
-// 40 KB for 384 clocks of MMA), small ones by streaming the experts' weights
-// from HBM once.
+// and accumulates in fp32; nothing is dequantised.
 //
-// Design (one CTA per SM, persistent, warp-specialised, 256 threads):
-//   warp 0     TMA producer: the tile's rows of A in boxes of 32 x 128 bytes
-//              (256 values of K; only as many boxes as the tile has rows), and
-//              B in units of 64 rows: 64 rows of W, or for gate_up 32 gate
-//              rows and the 32 up rows of the same features (one box of a 4-D
-//              map), so a unit holds both halves of 32 outputs.
-//   warp 1     TMEM allocator and MMA issuer: per step it copies the step's
-//              scales from shared memory to TMEM (tcgen05.cp) and issues up to
-//              four MMAs, M 128, N 64 per unit. Two accumulators.
-//   warps 2, 3 scale producers for A and B: the tensor core wants the four
-//              scale bytes of a row's 128 values as one word, row r at lane
-//              r % 32 and column r / 32. A lane loads 16 scale bytes (512
-//              values) of its rows r, r+32, ... from their plain row-major
-//              places and stores the transposed words, so neither rows nor
-//              weights need a layout of their own and a segment may start at
-//              any row.
-//   warps 4..7 epilogue: TMEM to registers, SwiGLU / rounding / quantisation
-//              of a lane's own row, 16-byte stores of 64-byte pieces through
-//              a swizzled staging buffer; rows past the segment are dropped.
-// A tile is 128 rows by 1..3 units. Every CTA picks the units per tile from the
-// number of row tiles, which only the device knows (choose_units). The ring's
-// stage size follows the units, and its depth the stage size.
+// What bounds it. Few rows: streaming the experts' weights from HBM once (gate_up
+// of 16 tokens, 256 experts, H 7168, I 2048: 1.6 GB in 242 us, 6.6 TB/s). Many
+// rows: shared memory, which takes the operands from L2 and gives them to the
+// tensor cores (at N 192 and 256 values of K, 28 KB in and some 40 KB out a
+// step of 384 MMA clocks, 128 bytes a clock), and the power limit, which holds
+// the SM clock near 1.5 GHz (gate_up of 8192 tokens, 64 experts, H 4096, I 2048:
+// 409 us, 4.0 PFLOP/s).
+//
+// Design (a CTA on each SM, persistent, warp-specialised, 480 threads):
+//   warp 0      TMA producer, 256 values of K a step: the tile's rows of A (one
+//               box of 128, or for a short tile as many of 32 as it has), and
+//               64 rows of W per unit of the tile; for gate_up 32 gate rows per
+//               unit and then the 32 up rows of the same features.
+//   warp 1      MMA issuer: up to four MMAs a step. Two accumulators.
+//   warp 2      copies the scales of two steps from shared memory to TMEM, into
+//               one of two sets of columns.
+//   warps 3-6   scale producers: the tensor core wants the four scale bytes of
+//               a row's 128 values as one word, row r at lane r % 32 and column
+//               r / 32. A lane loads 16 scale bytes (512 values) of its rows r,
+//               r+32, ... from their plain row-major places and stores the
+//               transposed words, so neither rows nor weights need a layout of
+//               their own and a segment may start at any row.
+//   warps 7-14  epilogue: TMEM to registers, SwiGLU / rounding / quantisation
+//               of a lane's own row, stores by TMA from a staging buffer.
+// A tile is 128 rows by 1..3 units, which every CTA picks from the number of
+// row tiles, known to the device only (choose_units); the ring's stages follow.
+// For large segments two CTAs share a tile of 256 rows by 3 units: each loads
+// its own rows of A and half of W's, and the leader's threads issue the MMAs
+// and scale copies of both (use_pairs says when).
 //
 // Waits are bounded as in gemm_tc.cu.
 #include <cuda.h>
@@ -510,8 +514,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- scales from shared memory to TMEM ----------------
-    // A thread of its own: the twelve copies of a vector would take the MMA's
-    // a third of its time.
+    // A thread of its own: twelve copies for every two steps took a third of the
+    // MMA issuer's time (420 us a gate_up that now takes 409).
     if (leader && elect_one()) {
       const int sf_bytes = sf_stage_bytes(units), n_vec = (args.k_steps + 1) / 2;
       const uint32_t sf_smem = smem_u32(sf_base);
@@ -552,9 +556,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     __syncwarp();
   } else if (warp < EPI_WARP0) {
     // ---------------- scale producers ----------------
-    // The warps take the vectors of the CTA's tiles in turn, each into a stage of
-    // its own, so that the loads of several are in flight. (One warp that loads ahead of what it stores
-    // gains nothing: its fence waits for all its loads.)
+    // The warps take the 512-value vectors of the CTA's tiles in turn, each into
+    // a stage of its own, so that the loads of several are in flight.
     constexpr int kA = BM / 32, kB = MAX_UNITS * UNIT / 32;  // rows of a lane
     const int n_vec = (args.k_steps + 1) / 2, stage = warp - SF_WARP0;
     uint8_t* const stage_base = sf_base + stage * sf_stage_bytes(units) + lane * 16;
@@ -828,13 +831,20 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   return cudaGetLastError();
 }
 
-bool use_pairs(int64_t rows, int64_t E, int64_t n_units) { return rows >= 512 * E && n_units >= MAX_UNITS; }
+// Pairs halve the traffic of W but fill 256-row tiles: they pay from about 512
+// rows an expert on (us, one CTA / pairs: 64 experts of N 4096, K 2048 at 256
+// rows each 105 / 104, at 512 171 / 165, at 1536 443 / 407; 128 experts of N
+// 2048, K 768 at 256 58 / 60, at 1536 242 / 227), and lose with few steps a
+// pair (gate_up of 16 experts, H 1024, I 512 at 768: 23.6 / 25.3).
+bool use_pairs(int64_t rows, int64_t E, int64_t n_units, int64_t k_steps) {
+  return rows >= 512 * E && rows / (2 * BM) * ceil_div(n_units, MAX_UNITS) * k_steps >= 64 * (num_sms() / 2);
+}
 
 template <int MODE>
 cudaError_t launch_product(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_data, const void* a_scale,
                            const int32_t* offsets, const void* w_data, const void* w_scale, void* out, void* out_scale,
                            int32_t* err, cudaStream_t s) {
-  const bool pairs = use_pairs(rows, E, ceil_div(N, is_swiglu(MODE) ? UNIT / 2 : UNIT));
+  const bool pairs = use_pairs(rows, E, ceil_div(N, is_swiglu(MODE) ? UNIT / 2 : UNIT), ceil_div(K, BK));
   return pairs ? launch<MODE, true>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, out_scale, err, s)
                : launch<MODE, false>(rows, E, N, K, a_data, a_scale, offsets, w_data, w_scale, out, out_scale, err, s);
 }

@@ -16,9 +16,15 @@
 // there is at most one multiply-add per element read. They are therefore cut
 // by token: a token's own row (x, dout, out) is read or written once, in
 // registers, and only its k sorted rows are touched besides it, each with
-// 16-byte accesses that cover whole lines. A thread first issues the loads of
-// up to eight sorted rows and then uses them in slot order.
+// 16-byte accesses that cover whole lines. What reaches the memory's rate is
+// the loads in flight, so the kernels are compiled for each k up to 8 (more
+// slots go eight at a time), and a thread issues those of several vectors of
+// its token before it uses the first: 8 for k 1, 4 for k 2 and 3, else 2.
+// (8192 x 8192 bf16, k 2: unpermute 130 us with one vector a thread.)
 #include <cuda_runtime.h>
+
+#include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -32,26 +38,22 @@ namespace {
 constexpr int RTHREADS = 256;
 constexpr int kSlots = 8;  // sorted rows of a token in flight at once
 
-// 16 bytes of a row as fp32: 4 fp32 or 8 bf16 values.
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float* f) {
-  const uint4 v = *reinterpret_cast<const uint4*>(p);
-  if constexpr (sizeof(T) == 4) unpack16(v, f, static_cast<float*>(nullptr));
-  else unpack16_bf16(v, f);
-}
-
-// The N values at p as fp32: 16 bytes, or 8 (four bf16 beside four fp32).
+// N values as they lie in memory: 16 bytes, or 8 (four bf16 beside four fp32).
 template <int N, typename T>
-__device__ __forceinline__ void loadn(const T* p, float* f) {
-  if constexpr (N * sizeof(T) == 16) {
-    load16(p, f);
-  } else {
+using Raw = std::conditional_t<N * sizeof(T) == 16, uint4, uint2>;
+
+template <int N, typename T>
+__device__ __forceinline__ void unpackn(const Raw<N, T>& v, float* f) {
+  if constexpr (N * sizeof(T) == 8) {
     static_assert(N == 4 && sizeof(T) == 2, "four bf16");
-    const uint2 v = *reinterpret_cast<const uint2*>(p);
     f[0] = __uint_as_float(v.x << 16);
     f[1] = __uint_as_float(v.x & 0xffff0000u);
     f[2] = __uint_as_float(v.y << 16);
     f[3] = __uint_as_float(v.y & 0xffff0000u);
+  } else if constexpr (sizeof(T) == 4) {
+    unpack16(v, f, static_cast<float*>(nullptr));
+  } else {
+    unpack16_bf16(v, f);
   }
 }
 
@@ -68,14 +70,30 @@ __device__ __forceinline__ void storen(T* p, const float* f) {
   }
 }
 
-// Sorted positions of a token's slots j0 .. j0+7; -1 for a slot past k, one
-// without a row, or (a plan that is not the dispatch's) one outside [0, P).
-__device__ __forceinline__ void load_slots(const int32_t* __restrict__ pp, int j0, int k, int64_t P, int (&p)[kSlots]) {
+// Sorted positions of a token's slots j0 .. j0 + SL - 1; -1 for a slot past k,
+// one without a row, or (a plan that is not the dispatch's) one outside [0, P).
+template <int SL>
+__device__ __forceinline__ void load_slots(const int32_t* __restrict__ pp, int j0, int k, int64_t P, int (&p)[SL]) {
 #pragma unroll
-  for (int j = 0; j < kSlots; ++j) {
+  for (int j = 0; j < SL; ++j) {
     p[j] = j0 + j < k ? __ldg(pp + j0 + j) : -1;
     if (p[j] >= P) p[j] = -1;
   }
+}
+
+// Their weights: 1 without a weight table, 0 for a slot without a row, which
+// adds nothing whatever its weight.
+template <int SL>
+__device__ __forceinline__ void load_weights(const float* __restrict__ w, int j0, const int (&p)[SL], float (&ww)[SL]) {
+#pragma unroll
+  for (int j = 0; j < SL; ++j) ww[j] = p[j] < 0 ? 0.f : w == nullptr ? 1.f : __ldg(w + j0 + j);
+}
+
+// A vector of a sorted row; zeros where there is none (selected, not branched
+// round, so that the loads of a thread go out together: branches around them
+// made 8192 x 2048 bf16, k 8, 87 us instead of 53).
+__device__ __forceinline__ uint4 load_row(const void* row, int v, bool has) {
+  return has ? __ldcs(static_cast<const uint4*>(row) + v) : make_uint4(0u, 0u, 0u, 0u);
 }
 
 // Zeroes the rows [offsets[E], P) of `rows` (nvec 16-byte vectors each).
@@ -87,34 +105,48 @@ __device__ __forceinline__ void zero_unused_rows(uint4* __restrict__ rows, const
     for (int v = threadIdx.x; v < nvec; v += RTHREADS) rows[r * nvec + v] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// A block is 256 >> lg token lanes of 1 << lg threads: a thread handles one
-// vector column of one token at a time, so no index needs a division.
+// A block is 256 >> lg teams of 1 << lg threads: a team handles one token at a
+// time, a thread V of its vectors a pass, so no index needs a division.
+template <int V>
 __global__ void __launch_bounds__(RTHREADS) permute_rows_kernel(const uint4* __restrict__ x,
                                                                 const int32_t* __restrict__ pair_pos,
                                                                 const int32_t* __restrict__ offsets,
                                                                 uint4* __restrict__ xs, int64_t Tn, int nvec, int k,
                                                                 int E, int lg) {
   const int64_t P = Tn * k;
-  const int tpb = RTHREADS >> lg, col = threadIdx.x & ((1 << lg) - 1);
+  const int tpb = RTHREADS >> lg, team = 1 << lg, col = threadIdx.x & (team - 1);
   for (int64_t t = (int64_t)blockIdx.x * tpb + (threadIdx.x >> lg); t < Tn; t += (int64_t)gridDim.x * tpb) {
     const int32_t* pp = pair_pos + t * k;
     int p[kSlots];
     load_slots(pp, 0, k, P, p);
-    for (int v = (blockIdx.y << lg) + col; v < nvec; v += gridDim.y << lg) {
-      const uint4 val = x[t * nvec + v];
+    for (int v0 = blockIdx.y * team * V + col; v0 < nvec; v0 += gridDim.y * team * V) {
+      uint4 val[V];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j)
-        if (p[j] >= 0) xs[(int64_t)p[j] * nvec + v] = val;
+      for (int i = 0; i < V; ++i)
+        if (v0 + i * team < nvec) val[i] = x[t * nvec + v0 + i * team];
+#pragma unroll
+      for (int j = 0; j < kSlots; ++j) {
+        if (p[j] < 0) continue;
+        uint4* o = xs + (int64_t)p[j] * nvec + v0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (v0 + i * team < nvec) o[i * team] = val[i];
+      }
       for (int j = kSlots; j < k; ++j) {
         const int q = __ldg(pp + j);
-        if (q >= 0 && q < P) xs[(int64_t)q * nvec + v] = val;
+        if (q < 0 || q >= P) continue;
+        uint4* o = xs + (int64_t)q * nvec + v0;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (v0 + i * team < nvec) o[i * team] = val[i];
       }
     }
   }
   zero_unused_rows(xs, offsets, E, P, nvec);
 }
 
-template <typename TY, typename TO, bool WEIGHTED>
+// SL: the token's slots, or 8 of them at a time.
+template <typename TY, typename TO, int SL, int V>
 __global__ void __launch_bounds__(RTHREADS) unpermute_rows_kernel(const TY* __restrict__ ys,
                                                                   const int32_t* __restrict__ pair_pos,
                                                                   const float* __restrict__ w,
@@ -124,155 +156,184 @@ __global__ void __launch_bounds__(RTHREADS) unpermute_rows_kernel(const TY* __re
   constexpr int N = 16 / sizeof(TY);
   const int64_t P = Tn * k;
   const int nvec = H / N;
-  const int tpb = RTHREADS >> lg, col = threadIdx.x & ((1 << lg) - 1);
+  const int tpb = RTHREADS >> lg, team = 1 << lg, col = threadIdx.x & (team - 1);
   for (int64_t t = (int64_t)blockIdx.x * tpb + (threadIdx.x >> lg); t < Tn; t += (int64_t)gridDim.x * tpb) {
-    int p0[kSlots];
-    float w0[kSlots];
-    load_slots(pair_pos + t * k, 0, k, P, p0);
-    if constexpr (WEIGHTED) {
+    const int32_t* pp = pair_pos + t * k;
+    const float* wt = w == nullptr ? nullptr : w + t * k;
+    int p0[SL];
+    float w0[SL];
+    load_slots(pp, 0, k, P, p0);
+    load_weights(wt, 0, p0, w0);
+    for (int v0 = blockIdx.y * team * V + col; v0 < nvec; v0 += gridDim.y * team * V) {
+      float acc[V][N];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) w0[j] = j < k ? __ldg(w + t * k + j) : 0.f;
-    }
-    for (int v = (blockIdx.y << lg) + col; v < nvec; v += gridDim.y << lg) {
-      float acc[N];
+      for (int i = 0; i < V; ++i)
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc[i] = 0.f;
-      auto add = [&](const int (&p)[kSlots], const float (&ww)[kSlots]) {
-        uint4 raw[kSlots];
+        for (int n = 0; n < N; ++n) acc[i][n] = 0.f;
+      auto add = [&](const int (&p)[SL], const float (&ww)[SL]) {
+        uint4 raw[V][SL];
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j)
-          if (p[j] >= 0) raw[j] = __ldcs(reinterpret_cast<const uint4*>(ys + (int64_t)p[j] * H) + v);
+        for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < kSlots; ++j) {
-          if (p[j] < 0) continue;  // a slot without a row adds nothing, whatever its weight
-          float f[N];
-          if constexpr (sizeof(TY) == 4) unpack16(raw[j], f, static_cast<float*>(nullptr));
-          else unpack16_bf16(raw[j], f);
+          for (int j = 0; j < SL; ++j)
+            raw[i][j] = load_row(ys + (int64_t)p[j] * H, v0 + i * team, p[j] >= 0 && v0 + i * team < nvec);
 #pragma unroll
-          for (int i = 0; i < N; ++i) acc[i] = WEIGHTED ? fmaf(ww[j], f[i], acc[i]) : acc[i] + f[i];
-        }
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < SL; ++j) {
+            float f[N];
+            unpackn<N, TY>(raw[i][j], f);
+#pragma unroll
+            for (int n = 0; n < N; ++n) acc[i][n] = fmaf(ww[j], f[n], acc[i][n]);
+          }
       };
       add(p0, w0);
-      for (int j0 = kSlots; j0 < k; j0 += kSlots) {
-        int p[kSlots];
-        float ww[kSlots];
-        load_slots(pair_pos + t * k, j0, k, P, p);
-        if constexpr (WEIGHTED) {
-#pragma unroll
-          for (int j = 0; j < kSlots; ++j) ww[j] = j0 + j < k ? __ldg(w + t * k + j0 + j) : 0.f;
-        }
-        add(p, ww);
-      }
-      if (shared_out != nullptr) {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-          const float4 s = __ldcs(reinterpret_cast<const float4*>(shared_out + t * H + v * N + i));
-          acc[i] += s.x;
-          acc[i + 1] += s.y;
-          acc[i + 2] += s.z;
-          acc[i + 3] += s.w;
+      if constexpr (SL == kSlots) {
+        for (int j0 = kSlots; j0 < k; j0 += kSlots) {
+          int p[SL];
+          float ww[SL];
+          load_slots(pp, j0, k, P, p);
+          load_weights(wt, j0, p, ww);
+          add(p, ww);
         }
       }
-      storen<N>(out + t * H + (int64_t)v * N, acc);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int v = v0 + i * team;
+        if (v >= nvec) break;
+        if (shared_out != nullptr) {
+#pragma unroll
+          for (int n = 0; n < N; n += 4) {
+            const float4 s = __ldcs(reinterpret_cast<const float4*>(shared_out + t * H + (int64_t)v * N + n));
+            acc[i][n] += s.x;
+            acc[i][n + 1] += s.y;
+            acc[i][n + 2] += s.z;
+            acc[i][n + 3] += s.w;
+          }
+        }
+        storen<N>(out + t * H + (int64_t)v * N, acc[i]);
+      }
     }
   }
 }
 
-// Sums eight values over a warp: afterwards the lanes with (lane & 3) == 0
-// hold the whole sum of value (lane >> 2). Each step halves what a lane
-// keeps, so eight sums take 9 shuffles instead of 40.
-__device__ __forceinline__ float warp_sum8(float (&a)[kSlots], int lane) {
+// The sums of SL values over a team of 1 << lt lanes of a warp, the whole sum
+// of value j in the team's lane j.
+template <int SL>
+__device__ __forceinline__ float team_sums(float (&a)[SL], int lt, int col) {
+  if constexpr (SL == kSlots) {
+    if (lt == 5) {
+      // Each step halves what a lane keeps: eight sums in 9 shuffles instead
+      // of 40, value (lane >> 2) in the lanes with (lane & 3) == 0, and one
+      // more to lane j.
 #pragma unroll
-  for (int n = 4, o = 16; n >= 1; n >>= 1, o >>= 1) {
-    const bool upper = lane & o;
+      for (int n = 4, o = 16; n >= 1; n >>= 1, o >>= 1) {
+        const bool upper = col & o;
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const float send = upper ? a[i] : a[i + n];
-      const float keep = upper ? a[i + n] : a[i];
-      a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        for (int i = 0; i < n; ++i) {
+          const float send = upper ? a[i] : a[i + n];
+          const float keep = upper ? a[i + n] : a[i];
+          a[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+      }
+      a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
+      a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
+      return __shfl_sync(0xffffffffu, a[0], (col & 7) << 2);
     }
   }
-  a[0] += __shfl_xor_sync(0xffffffffu, a[0], 2);
-  a[0] += __shfl_xor_sync(0xffffffffu, a[0], 1);
-  return a[0];
+  float mine = 0.f;
+#pragma unroll
+  for (int j = 0; j < SL; ++j) {
+    for (int o = 1 << lt >> 1; o >= 1; o >>= 1) a[j] += __shfl_xor_sync(0xffffffffu, a[j], o);
+    if (col == j) mine = a[j];
+  }
+  return mine;
 }
 
-// 1 << lw warps share one token's columns, and its slots are taken eight at a
-// time. dys and dw may each be absent.
-template <typename TY, typename TD>
+// 1 << lt threads (8 to 256) share one token's columns, and its slots are taken
+// SL at a time. dys and dw may each be absent.
+template <typename TY, typename TD, int SL, int V>
 __global__ void __launch_bounds__(RTHREADS) unpermute_rows_backward_kernel(
     const TD* __restrict__ dout, const TY* __restrict__ ys, const int32_t* __restrict__ pair_pos,
     const int32_t* __restrict__ offsets, const float* __restrict__ w, TY* __restrict__ dys, float* __restrict__ dw,
-    int64_t Tn, int H, int k, int E, int lw) {
+    int64_t Tn, int H, int k, int E, int lt) {
   constexpr int N = 16 / sizeof(TY);
   __shared__ float part[RTHREADS / 32][kSlots];
   const int64_t P = Tn * k;
   const int nvec = H / N;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tpb = (RTHREADS / 32) >> lw, team = 32 << lw;
+  const int warp = threadIdx.x >> 5;
+  const int tpb = RTHREADS >> lt, team = 1 << lt, col = threadIdx.x & (team - 1);
   for (int64_t tb = (int64_t)blockIdx.x * tpb; tb < Tn; tb += (int64_t)gridDim.x * tpb) {
-    const int64_t t = tb + (warp >> lw);
+    const int64_t t = tb + (threadIdx.x >> lt);
     const bool live = t < Tn;
-    for (int j0 = 0; j0 < k; j0 += kSlots) {
-      int p[kSlots];
-      float ww[kSlots], acc[kSlots];
+    for (int j0 = 0; j0 < k; j0 += SL) {
+      int p[SL];
+      float ww[SL], acc[SL];
 #pragma unroll
-      for (int j = 0; j < kSlots; ++j) {
+      for (int j = 0; j < SL; ++j) {
         p[j] = -1;
         ww[j] = 1.f;
         acc[j] = 0.f;
       }
       if (live) {
         load_slots(pair_pos + t * k, j0, k, P, p);
-        if (w != nullptr) {
+        load_weights(w == nullptr ? nullptr : w + t * k, j0, p, ww);
+        for (int v0 = col; v0 < nvec; v0 += team * V) {
+          Raw<N, TD> draw[V];
+          uint4 raw[V][SL];
 #pragma unroll
-          for (int j = 0; j < kSlots; ++j) ww[j] = j0 + j < k ? __ldg(w + t * k + j0 + j) : 0.f;
-        }
-        for (int v = threadIdx.x & (team - 1); v < nvec; v += team) {
-          float d[N];
-          loadn<N>(dout + t * H + (int64_t)v * N, d);
-          uint4 raw[kSlots];
-          if (dw != nullptr) {
+          for (int i = 0; i < V; ++i) {
+            const int v = v0 + i * team;
+            draw[i] = v < nvec ? *reinterpret_cast<const Raw<N, TD>*>(dout + t * H + (int64_t)v * N) : Raw<N, TD>{};
+            if (dw != nullptr) {
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j)
-              if (p[j] >= 0) raw[j] = __ldcs(reinterpret_cast<const uint4*>(ys + (int64_t)p[j] * H) + v);
-          }
-          if (dys != nullptr) {
-#pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
-              if (p[j] < 0) continue;
-              float g[N];
-#pragma unroll
-              for (int i = 0; i < N; ++i) g[i] = ww[j] * d[i];
-              storen<N>(dys + (int64_t)p[j] * H + (int64_t)v * N, g);
+              for (int j = 0; j < SL; ++j)
+                raw[i][j] = load_row(ys + (int64_t)p[j] * H, v, p[j] >= 0 && v < nvec);
             }
           }
-          if (dw != nullptr) {
 #pragma unroll
-            for (int j = 0; j < kSlots; ++j) {
-              if (p[j] < 0) continue;
-              float f[N];
-              if constexpr (sizeof(TY) == 4) unpack16(raw[j], f, static_cast<float*>(nullptr));
-              else unpack16_bf16(raw[j], f);
+          for (int i = 0; i < V; ++i) {
+            const int v = v0 + i * team;
+            if (v >= nvec) break;
+            float d[N];
+            unpackn<N, TD>(draw[i], d);
+            if (dys != nullptr) {
 #pragma unroll
-              for (int i = 0; i < N; ++i) acc[j] = fmaf(d[i], f[i], acc[j]);
+              for (int j = 0; j < SL; ++j) {
+                float g[N];
+#pragma unroll
+                for (int n = 0; n < N; ++n) g[n] = ww[j] * d[n];
+                if (p[j] >= 0) storen<N>(dys + (int64_t)p[j] * H + (int64_t)v * N, g);
+              }
+            }
+            if (dw != nullptr) {
+#pragma unroll
+              for (int j = 0; j < SL; ++j) {
+                float f[N];
+                unpackn<N, TY>(raw[i][j], f);
+#pragma unroll
+                for (int n = 0; n < N; ++n) acc[j] = fmaf(d[n], f[n], acc[j]);
+              }
             }
           }
         }
+#pragma unroll
+        for (int j = 0; j < SL; ++j)
+          if (p[j] < 0) acc[j] = 0.f;  // dout may hold an infinity
       }
       if (dw != nullptr) {  // the same for the whole block
-        const float s = warp_sum8(acc, lane);
-        const int j = lane >> 2;
-        if (lw == 0) {
-          if (live && (lane & 3) == 0 && j0 + j < k) dw[t * k + j0 + j] = s;
+        if (lt <= 5) {
+          const float s = team_sums(acc, lt, col);
+          if (live && col < SL && j0 + col < k) dw[t * k + j0 + col] = s;
         } else {
-          if ((lane & 3) == 0) part[warp][j] = s;
+          const int lane = threadIdx.x & 31;
+          const float s = team_sums(acc, 5, lane);
+          if (lane < SL) part[warp][lane] = s;
           __syncthreads();
-          const int first = warp & ~((1 << lw) - 1);
-          if (live && warp == first && lane < kSlots && j0 + lane < k) {
+          if (live && col < SL && j0 + col < k) {
             float sum = 0.f;
-            for (int i = 0; i < (1 << lw); ++i) sum += part[first + i][lane];
-            dw[t * k + j0 + lane] = sum;
+            for (int i = 0; i < team >> 5; ++i) sum += part[warp + i][col];
+            dw[t * k + j0 + col] = sum;
           }
           __syncthreads();
         }
@@ -291,37 +352,59 @@ moe_status check_problem(const moe_problem* p) {
   return moe_workspace_size(p, &bytes);  // validates the problem
 }
 
-// log2 of the threads a token lane gets: the most (up to 256) that leave at
-// most a quarter of them idle on the last pass over nvec vectors, and never
-// fewer than 4.
-int lane_log2(int64_t nvec) {
+// Vectors of a token that a thread takes at once for SL slots.
+constexpr int vectors_for(int SL) { return SL == 1 ? 8 : SL <= 3 ? 4 : 2; }
+
+// Several vectors a thread once that leaves 512 threads for each of 148 SMs:
+// few tokens need the threads more (300 tokens of 2048 bf16, k 6: 4.6 us with
+// two vectors, 4.1 with one; 1024 tokens, k 8: 9.3 and 10.1).
+bool many(int64_t T, int64_t nvec, int V) { return T * nvec >= (int64_t)V * 148 * 512; }
+
+// log2 of a team's threads for `passes` vectors (or groups of them): the most
+// (up to 256) that leave at most a quarter of them idle on the last pass, and
+// never fewer than 4.
+int lane_log2(int64_t passes) {
   int lg = 8;
-  while (lg > 2 && round_up(nvec, int64_t(1) << lg) * 4 > nvec * 5) --lg;
+  while (lg > 2 && round_up(passes, int64_t(1) << lg) * 4 > passes * 5) --lg;
   return lg;
 }
 
-// Blocks for T tokens in lanes of 1 << lg threads: full residency (eight
-// blocks of 256 threads on each of 148 SMs), split over the columns too when
-// the tokens alone give fewer.
-dim3 lane_grid(int64_t T, int64_t nvec, int lg) {
-  const int64_t full = 148 * 8;
+// Blocks for T tokens in teams of 1 << lg threads: at most `most`, and split
+// over the columns too when the tokens alone give less than full residency
+// (eight blocks of 256 threads on each of 148 SMs).
+constexpr int64_t kResident = 148 * 8;
+dim3 lane_grid(int64_t T, int64_t passes, int lg, int64_t most) {
   const int64_t bx = ceil_div(T, RTHREADS >> lg);
-  const int64_t by = std::max<int64_t>(1, std::min<int64_t>(ceil_div(nvec, int64_t(1) << lg), full / std::max<int64_t>(1, bx)));
-  return dim3((unsigned)std::min(bx, full), (unsigned)by);
+  const int64_t by =
+      std::max<int64_t>(1, std::min<int64_t>(ceil_div(passes, int64_t(1) << lg), kResident / std::max<int64_t>(1, bx)));
+  return dim3((unsigned)std::min(bx, most), (unsigned)by);
+}
+
+// f(slots) for the smallest compiled number of slots that takes k at once.
+template <int SL = 1, typename F>
+void with_slots(int64_t k, F&& f) {
+  if constexpr (SL == kSlots) f(std::integral_constant<int, SL>{});
+  else if (k <= SL) f(std::integral_constant<int, SL>{});
+  else with_slots<SL + 1>(k, f);
 }
 
 template <typename TY, typename TO>
 cudaError_t launch_unpermute(const void* ys, const int32_t* pair_pos, const float* w, const float* shared_out,
                              void* out, int64_t T, int64_t H, int64_t k, cudaStream_t s) {
   const int64_t nvec = H * sizeof(TY) / 16;
-  const int lg = lane_log2(nvec);
-  const dim3 grid = lane_grid(T, nvec, lg);
-  if (w != nullptr)
-    unpermute_rows_kernel<TY, TO, true><<<grid, RTHREADS, 0, s>>>(
-        static_cast<const TY*>(ys), pair_pos, w, shared_out, static_cast<TO*>(out), T, (int)H, (int)k, lg);
-  else
-    unpermute_rows_kernel<TY, TO, false><<<grid, RTHREADS, 0, s>>>(
-        static_cast<const TY*>(ys), pair_pos, w, shared_out, static_cast<TO*>(out), T, (int)H, (int)k, lg);
+  with_slots(k, [&](auto slots) {
+    // twice as many of fp32, whose vectors have half the values to sum
+    constexpr int SL = decltype(slots)::value;
+    constexpr int V = vectors_for(SL) * (sizeof(TY) == 4 && SL > 1 && SL < kSlots ? 2 : 1);
+    auto launch = [&](auto kernel, int per_thread) {
+      const int64_t passes = ceil_div(nvec, per_thread);
+      const int lg = lane_log2(passes);
+      kernel<<<lane_grid(T, passes, lg, kResident), RTHREADS, 0, s>>>(static_cast<const TY*>(ys), pair_pos, w, shared_out,
+                                                          static_cast<TO*>(out), T, (int)H, (int)k, lg);
+    };
+    if (many(T, nvec, V)) launch(unpermute_rows_kernel<TY, TO, SL, V>, V);
+    else launch(unpermute_rows_kernel<TY, TO, SL, 1>, 1);
+  });
   return cudaGetLastError();
 }
 
@@ -330,14 +413,24 @@ cudaError_t launch_unpermute_backward(const void* dout, const void* ys, const in
                                       const int32_t* offsets, const float* w, void* dys, float* dw, int64_t T,
                                       int64_t H, int64_t k, int64_t E, cudaStream_t s) {
   const int64_t nvec = H * sizeof(TY) / 16;
-  // One warp per token while that alone fills the GPU (64 warps on each of
-  // 148 SMs); more warps for fewer tokens, as long as each has a vector.
-  int lw = 0;
-  while (lw < 3 && (T << lw) < 148 * 64 && nvec > (32 << lw)) ++lw;
-  const int64_t grid = std::min<int64_t>(ceil_div(T, 8 >> lw), 148 * 8);
-  unpermute_rows_backward_kernel<TY, TD><<<(unsigned)grid, RTHREADS, 0, s>>>(
-      static_cast<const TD*>(dout), static_cast<const TY*>(ys), pair_pos, offsets, w, static_cast<TY*>(dys), dw, T,
-      (int)H, (int)k, (int)E, lw);
+  with_slots(k, [&](auto slots) {
+    // half as many where each load is answered by a store
+    constexpr int SL = decltype(slots)::value, V = std::max(2, vectors_for(SL) / 2);
+    auto launch = [&](auto kernel, int per_thread) {
+      // A warp per token, or for short rows less (8 lanes at least: a lane
+      // writes each slot's weight gradient); more for few tokens, as long as
+      // each thread has a vector.
+      const int64_t passes = ceil_div(nvec, per_thread);
+      int lt = 5;
+      while (lt > 3 && (int64_t(1) << lt) >= 2 * passes) --lt;
+      while (lt >= 5 && lt < 8 && (T << lt) < 148 * 2048 && passes > (int64_t(1) << lt)) ++lt;
+      const int64_t grid = std::min<int64_t>(ceil_div(T, RTHREADS >> lt), 148 * 8);
+      kernel<<<(unsigned)grid, RTHREADS, 0, s>>>(static_cast<const TD*>(dout), static_cast<const TY*>(ys), pair_pos,
+                                                 offsets, w, static_cast<TY*>(dys), dw, T, (int)H, (int)k, (int)E, lt);
+    };
+    if (many(T, nvec, V)) launch(unpermute_rows_backward_kernel<TY, TD, SL, V>, V);
+    else launch(unpermute_rows_backward_kernel<TY, TD, SL, 1>, 1);
+  });
   return cudaGetLastError();
 }
 
@@ -353,10 +446,19 @@ MOE_API moe_status moe_permute_rows(const moe_problem* p, const void* x, const i
   if (p->T == 0) return MOE_OK;
   if (!ok_ptr(x) || !ok_ptr(pair_pos) || !ok_ptr(offsets) || !ok_ptr(x_perm)) return MOE_ERR_INVALID_ARGUMENT;
   const int64_t nvec = p->H * (p->dtype == MOE_DTYPE_F32 ? 4 : 2) / 16;
-  const int lg = lane_log2(nvec);
-  permute_rows_kernel<<<lane_grid(p->T, nvec, lg), RTHREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      static_cast<const uint4*>(x), pair_pos, offsets, static_cast<uint4*>(x_perm), p->T, (int)nvec, (int)p->k,
-      (int)p->E, lg);
+  auto launch = [&](auto kernel, int per_thread) {
+    const int64_t passes = ceil_div(nvec, per_thread);
+    const int lg = lane_log2(passes);
+    // Blocks that end early are replaced as they end, which evens out the stores
+    // (8192 x 2048 bf16, k 8: 54 us with resident blocks, 49 so); with k 1 there
+    // is nothing to even out (20.7 and 22.7 us of 8192 x 4096).
+    kernel<<<lane_grid(p->T, passes, lg, p->k == 1 ? kResident : kResident * 64), RTHREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+        static_cast<const uint4*>(x), pair_pos, offsets, static_cast<uint4*>(x_perm), p->T, (int)nvec, (int)p->k,
+        (int)p->E, lg);
+  };
+  // each load is followed by k stores: few of those leave the loads' time bare
+  if (p->k <= 4 && many(p->T, nvec, 4)) launch(permute_rows_kernel<4>, 4);
+  else launch(permute_rows_kernel<1>, 1);
   return cudaGetLastError() == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
