@@ -857,7 +857,7 @@ moe_status check_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, int64_t n_
   if (rows < 0 || rows >= lim || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= lim)
     return MOE_ERR_INVALID_ARGUMENT;
   if (K % mx4::kBlock != 0 || N % n_multiple != 0) return MOE_ERR_INVALID_ARGUMENT;
-  if ((rows / BM + E) * ceil_div(N, 32) >= lim) return MOE_ERR_INVALID_ARGUMENT;
+  if ((rows / BM + E) * ceil_div(N, 32) >= lim - 4096) return MOE_ERR_INVALID_ARGUMENT;  // a round of tiles beyond
   return MOE_OK;
 }
 

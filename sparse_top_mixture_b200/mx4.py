@@ -12,7 +12,8 @@ power-of-two scale (``include/moe.h`` gives the format and the rounding).
     y = stm.mx4_grouped_matmul(h, down, plan["offsets"])
     out = stm.unpermute_rows(p, y, plan, routing_weights)
 
-``Mx4SparseMoE`` is that as a layer, called like ``SparseMoE``.
+``Mx4SparseMoE`` is that as a layer, called like ``SparseMoE``. Nothing here
+takes part in autograd.
 """
 
 from __future__ import annotations
@@ -22,9 +23,8 @@ from typing import Dict, Optional, Sequence, Tuple
 
 import torch
 
-from . import (DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, dispatch, lib, new_workspace, route,
-               shared_expert)
-from .rows import _plan, _same_device, unpermute_rows
+from . import DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, lib, new_workspace
+from .rows import _plan, _same_device
 
 _DTYPE_ID = {TORCH_DTYPE[name]: i for name, i in DTYPES.items()}
 
@@ -179,7 +179,7 @@ class Mx4SparseMoE(SparseMoE):
     products. ``weights`` as there; gate_up and down in the problem's dtype
     (quantised here, once) or as ``Mx4``. The router and the shared expert keep
     their weights; the shared expert runs on the caller's stream. bf16
-    problems, H and I multiples of 32."""
+    problems, H and I multiples of 32. For inference: it has no backward pass."""
 
     def __init__(self, p: Problem, weights: Dict[str, Optional[torch.Tensor]], device="cuda",
                  overlap_shared: bool = False):
@@ -195,44 +195,64 @@ class Mx4SparseMoE(SparseMoE):
             if not isinstance(w[name], Mx4):
                 _req(w[name], name, shape, dt)
                 w[name] = mx4_quantize(w[name])
-            _req_mx4(w[name], name, shape[:2])
-            if w[name].K != shape[2]:
+            if _req_mx4(w[name], name, shape[:2]) != shape[2]:
                 raise ValueError(f"{name}: K {w[name].K}, expected {shape[2]}")
         _req(w["gate_w"], "gate_w", (p.E, p.H), dt)
         if (p.bias_mode != "none") != (w.get("bias") is not None):
             raise ValueError("a bias goes with bias_mode 'logit' or 'select'")
+        if w.get("bias") is not None:
+            _req(w["bias"], "bias", (p.E,), torch.float32)
         if (p.shared == "sigmoid_gated") != (w.get("shared_gate") is not None):
             raise ValueError("shared_gate goes with shared 'sigmoid_gated'")
+        if w.get("shared_gate") is not None:
+            _req(w["shared_gate"], "shared_gate", (p.H,), dt)
+        if p.shared != "none":
+            _req(w["shared_gate_up"], "shared_gate_up", (2 * p.I_shared, p.H), dt)
+            _req(w["shared_down"], "shared_down", (p.H, p.I_shared), dt)
         self.p, self.w = p, w
         self.device = torch.device(device)
         self.ws = new_workspace(p, self.device)
         self.aux = None
         self._counts = torch.zeros(p.E, dtype=torch.int32, device=self.device)
+        experts = {name: w[name].data for name in ("gate_up", "down")}
+        others = {name: w.get(name) for name in ("gate_w", "bias", "shared_gate", "shared_gate_up", "shared_down")}
+        _same_device(self.ws.device, **experts, **others)
 
     def forward(self, x, out=None, routing_weights=None, selected_experts=None, events=None):
         """out, routing_weights, selected_experts = moe(x), as SparseMoE's."""
         if events is not None:
             raise ValueError("stage events are recorded by SparseMoE only")
-        p, w = self.p, self.w
-        rw, sel, gamma = route(p, x, w["gate_w"], w.get("bias"), w.get("shared_gate"), ws=self.ws)
-        plan = dispatch(p, sel, ws=self.ws)
-        self._counts = plan["counts"]
-        rows = mx4_permute_rows(p, x, plan)
-        h = mx4_grouped_gate_up(rows, w["gate_up"], plan["offsets"], quantize=True, ws=self.ws)
-        y = mx4_grouped_matmul(h, w["down"], plan["offsets"], ws=self.ws)
+        p, w, ws = self.p, self.w, self.ws
+        out, rw, sel = self._outputs(x, out, routing_weights, selected_experts)
+        _req(out, "out", (p.T, p.H), torch.bfloat16)
+        _req(rw, "routing_weights", (p.T, p.k), torch.float32)
+        _req(sel, "selected_experts", (p.T, p.k), torch.int64)
+        dev = ws.device
+        _same_device(dev, x=x, out=out, routing_weights=rw, selected_experts=sel)
+        gate = w.get("shared_gate")
+        gamma = None if gate is None else torch.empty(p.T, dtype=torch.float32, device=dev)
+        _launch(lib().moe_route, dev, p.c(), x.data_ptr(), w["gate_w"].data_ptr(), _ptr(w.get("bias")), _ptr(gate),
+                rw.data_ptr(), sel.data_ptr(), _ptr(gamma), ws.data_ptr(), ws.numel())
+        # the counts stay in one buffer, so that a replayed graph's are the last forward's too
+        table = torch.empty(p.E + 1, dtype=torch.int32, device=dev)
+        pairs, pos = (torch.empty(p.T * p.k, dtype=torch.int32, device=dev) for _ in range(2))
+        _launch(lib().moe_dispatch, dev, p.c(), sel.data_ptr(), None, self._counts.data_ptr(), table.data_ptr(),
+                pairs.data_ptr(), pos.data_ptr(), None, ws.data_ptr(), ws.numel())
+        rows = mx4_permute_rows(p, x, {"pair_pos": pos, "offsets": table})
+        h = mx4_grouped_gate_up(rows, w["gate_up"], table, quantize=True, ws=ws)
+        y = mx4_grouped_matmul(h, w["down"], table, ws=ws)
         shared = None
         if p.shared != "none":
-            shared = shared_expert(p, x, w["shared_gate_up"], w["shared_down"], gamma, ws=self.ws)
-        with torch.no_grad():
-            got = unpermute_rows(p, y, plan, rw, shared)
-        for given, made in ((out, got), (routing_weights, rw), (selected_experts, sel)):
-            if given is not None:
-                given.copy_(made)
-        return (got if out is None else out, rw if routing_weights is None else routing_weights,
-                sel if selected_experts is None else selected_experts)
+            shared = torch.empty(p.T, p.H, dtype=torch.float32, device=dev)
+            _launch(lib().moe_shared_expert, dev, p.c(), x.data_ptr(), w["shared_gate_up"].data_ptr(),
+                    w["shared_down"].data_ptr(), _ptr(gamma), shared.data_ptr(), ws.data_ptr(), ws.numel())
+        _launch(lib().moe_unpermute_rows, dev, p.c(), DTYPES["bf16"], y.data_ptr(), pos.data_ptr(), rw.data_ptr(),
+                _ptr(shared), out.data_ptr())
+        return out, rw, sel
 
     __call__ = forward
 
     def forward_counts(self) -> torch.Tensor:
-        """Per-expert counts [E] int32 of the last forward."""
+        """Per-expert counts [E] int32 of the last forward (overwritten by the
+        next one)."""
         return self._counts

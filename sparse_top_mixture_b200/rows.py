@@ -12,6 +12,12 @@ their gradients as plain calls. The plan is what ``dispatch`` or
     rows = stm.permute_rows(p, x, plan)                 # [T*k, H], by expert
     y = my_experts(rows, plan["offsets"])
     out = stm.unpermute_rows(p, y, plan, routing_weights)
+
+Forward and backward can be captured in a CUDA graph. Capture ``backward()``
+only while no eager graph of the same leaves is alive (drop its outputs
+first), or take the gradients with ``torch.autograd.grad``: autograd adds a
+leaf's gradient on the stream of the first graph that it is part of, which a
+capture on another stream does not survive.
 """
 
 from __future__ import annotations

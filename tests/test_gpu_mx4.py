@@ -10,7 +10,7 @@ so K/32 + 2 such steps bound it. Rounding to bf16 adds 2^-8 of the value. SwiGLU
 |d silu/dg| <= 1.1, and exp, the division and the products in fp32 lose at most
 2^-20 of the result."""
 
-import ctypes
+import random
 
 import pytest
 import torch
@@ -221,6 +221,136 @@ def test_grouped_gate_up(rows, E, I, H, kind):
     assert torch.equal(q.data[used], want.data) and torch.equal(q.scale[used], want.scale)
 
 
+# Segments of 1, 2, 31 ... 257 rows and of none beside large ones: every fill of a tile of 128 and of 256 rows.
+LENGTHS = [0, 1, 2, 31, 32, 33, 0, 96, 97, 127, 128, 129, 160, 255, 256, 257, 384, 385]
+
+
+def _lengths(rows, E):
+    """Segments of LENGTHS and then equal ones, over all rows."""
+    n = LENGTHS + [0] * (E - len(LENGTHS))
+    rest = rows - sum(LENGTHS)
+    for e in range(len(LENGTHS), E):
+        n[e] = rest // (E - e)
+        rest -= n[e]
+    return torch.tensor([0] + n, dtype=torch.int32).cumsum(0).int()
+
+
+# Both sides of the rule for pairs of CTAs (512 rows an expert and 64 steps a pair), with columns that end inside a
+# unit, a tile of three units and 16 bytes, and K that ends inside a step and an MMA
+@pytest.mark.parametrize("rows,E,N,K", [(3500, 20, 1096, 2080), (11000, 20, 1096, 2080), (11000, 20, 712, 3232),
+                                        (24000, 24, 200, 4128), (40000, 30, 2048, 512)])
+def test_segments_of_every_length(rows, E, N, K):
+    a, w = _operands(rows, E, N, K, seed=rows + N)
+    off = _lengths(rows, E)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    ref, mag = _product(a, w, off)
+    for dtype in (torch.float32, torch.bfloat16):
+        got = stm.mx4_grouped_matmul(a, w, off.cuda(), dtype, ws=ws)
+        bound = _steps(K) * mag + (2.0 ** -8 * ref.abs() if dtype == torch.bfloat16 else 0)
+        assert bool(((got.double() - ref).abs() <= bound).all())
+    assert stm.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("rows,E,I,H", [(3500, 20, 544, 2080), (11000, 20, 544, 2080), (24000, 24, 96, 4128),
+                                        (40000, 30, 1024, 512)])
+def test_gate_up_of_segments_of_every_length(rows, E, I, H):
+    a, w = _operands(rows, E, 2 * I, H, seed=rows + I)
+    off = _lengths(rows, E)
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    got = stm.mx4_grouped_gate_up(a, w, off.cuda(), ws=ws)
+    y, mag = _product(a, w, off)
+    g, u, dg, du = y[:, :I], y[:, I:], _steps(H) * mag[:, :I], _steps(H) * mag[:, I:]
+    silu = g * torch.sigmoid(g)
+    ref = silu * u
+    slack = 1.1 * dg * (u.abs() + du) + silu.abs() * du
+    assert bool(((got.double() - ref).abs() <= slack + (2.0 ** -8 + 2.0 ** -20) * (ref.abs() + slack)).all())
+    q = stm.mx4_grouped_gate_up(a, w, off.cuda(), quantize=True, ws=ws)
+    want = stm.mx4_quantize(got)
+    assert torch.equal(q.data, want.data) and torch.equal(q.scale, want.scale)
+    assert stm.read_device_error(ws) == 0
+
+
+@pytest.mark.parametrize("seed", range(12))
+def test_random_products(seed):
+    r = random.Random(seed)
+    E = r.choice([1, 3, 8, 60, 128, 256])
+    N, K = 8 * r.randint(1, 160), 32 * r.randint(1, 70)
+    rows = int(2 ** r.uniform(0, 14))
+    a, w = _operands(rows, E, N, K, seed=100 + seed)
+    off = _offsets(rows, E, seed, r.choice(["spread", "short", "one"]))
+    got = stm.mx4_grouped_matmul(a, w, off.cuda(), torch.float32)
+    ref, mag = _product(a, w, off)
+    used = slice(int(off[0]), int(off[E]))
+    assert bool(((got.double() - ref).abs() <= _steps(K) * mag)[used].all())
+    I = 32 * r.randint(1, 30)
+    a, w = _operands(rows, E, 2 * I, K, seed=200 + seed)
+    got = stm.mx4_grouped_gate_up(a, w, off.cuda())
+    y, mag = _product(a, w, off)
+    g, u, dg, du = y[:, :I], y[:, I:], _steps(K) * mag[:, :I], _steps(K) * mag[:, I:]
+    silu = g * torch.sigmoid(g)
+    slack = 1.1 * dg * (u.abs() + du) + silu.abs() * du
+    bound = slack + (2.0 ** -8 + 2.0 ** -20) * ((silu * u).abs() + slack)
+    assert bool(((got.double() - silu * u).abs() <= bound)[used].all())
+
+
+def test_swiglu_far_from_zero():
+    """Gates of large magnitude on both sides, zeros, and products that overflow: as the formula in fp32 has them."""
+    values = torch.tensor([0.0, -0.0, 1e-30, -1e-30, 1.0, -1.0, 20.0, -20.0, 87.0, -87.0, -88.5, 89.0, -104.0, 3e4, -3e4,
+                           1e30, -1e30, 3e38, -3e38])
+    # one row whose products with W are exactly the values: x = e_0 in the first block of 32
+    rows, I, H = 1, 32, 32
+    x = torch.zeros(rows, H)
+    x[0, 0] = 1.0
+    for gate in values.tolist():
+        q = stm.mx4_quantize(torch.full((1, 32), gate).cuda()).dequantize(torch.float32)[0, 0].double().cpu()
+        wt = torch.zeros(1, 2 * I, H)
+        wt[0, :I, 0], wt[0, I:, 0] = gate, 1.0
+        off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        got = stm.mx4_grouped_gate_up(stm.mx4_quantize(x.cuda()), stm.mx4_quantize(wt.cuda()), off).double().cpu()
+        ref = q * torch.sigmoid(q)
+        assert bool(((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref.abs() + 2.0 ** -119 * q.abs() + 2.0 ** -133).all()), gate
+
+
+def test_two_products_at_once_and_replayed():
+    """Two streams that run products of different sizes at the same time, and the same from graphs that share a
+    workspace."""
+    sizes = [(4000, 6, 1096, 1056, 1), (64, 16, 4096, 2048, 2)]
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    runs = []
+    for rows, E, N, K, seed in sizes:
+        a, w = _operands(rows, E, N, K, seed)
+        off = _offsets(rows, E, seed).cuda()
+        runs.append((a, w, off, stm.mx4_grouped_matmul(a, w, off, torch.float32, ws=ws)))
+    streams = [torch.cuda.Stream() for _ in sizes]
+    torch.cuda.synchronize()
+    results = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                results[i].append(stm.mx4_grouped_matmul(*runs[i][:3], torch.float32, ws=ws))
+    torch.cuda.synchronize()
+    for (_, _, _, want), got in zip(runs, results):
+        assert all(torch.equal(g, want) for g in got)
+    graphs, held = [], []
+    for (a, w, off, _), s in zip(runs, streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            held.append(stm.mx4_grouped_matmul(a, w, off, torch.float32, ws=ws))
+        graphs.append(g)
+    for (a, *_), s in zip(runs, streams):
+        a.data.copy_(a.data.flip(0))
+        a.scale.copy_(a.scale.flip(0))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (a, w, off, _), got in zip(runs, held):
+        assert torch.equal(got, stm.mx4_grouped_matmul(a, w, off, torch.float32))
+    assert stm.read_device_error(ws) == 0
+
+
 def test_products_are_the_same_every_time():
     a, w = _operands(3000, 6, 704, 1056, 5)
     off = _offsets(3000, 6, 5).cuda()
@@ -375,6 +505,24 @@ def test_layer_in_a_graph_and_in_the_host_pipeline():
         assert torch.equal(host_out, want[0].cpu())
 
 
+def test_layer_counts_after_a_replay_are_the_replays():
+    p, dev, moe = _layer("dsv4")
+    x = dev["x"].clone()
+    g = stm.GraphedForward(moe, x)
+    moe(dev["x"].flip(1).contiguous())  # an eager forward in between
+    _, _, sel = g.replay()
+    assert torch.equal(moe.forward_counts(), torch.bincount(sel.reshape(-1), minlength=p.E).int())
+
+
+def test_layer_without_tokens():
+    p, dev, _ = _layer("dsv4")
+    p0 = stm.Problem(**{**p.__dict__, "T": 0})
+    moe = stm.Mx4SparseMoE(p0, dev)
+    out, rw, sel = moe(dev["x"][:0].contiguous())
+    assert out.shape == (0, p.H) and rw.shape == (0, p.k) and sel.shape == (0, p.k)
+    assert int(moe.forward_counts().sum()) == 0 and moe.read_device_error() == 0
+
+
 def test_layer_with_the_balancer_and_given_outputs():
     p, dev, moe = _layer("dsv4")
     bal = stm.BiasBalancer(moe, 1e-3)
@@ -445,6 +593,14 @@ def test_refusals():
            lambda: stm.mx4_permute_rows(p, x.float(), plan),
            lambda: stm.Mx4SparseMoE(stm.Problem(T=4, H=64, E=2, k=1, I=32, dtype="f32"), {}),
            lambda: stm.Mx4SparseMoE(stm.Problem(T=4, H=64, E=2, k=1, I=40), {})]
+    p, dev, moe = _layer("dsv4")
+    half = dev["x"].half()
+    bad += [lambda: moe(half), lambda: moe(dev["x"], out=half), lambda: moe(dev["x"][1:]),
+            lambda: moe(dev["x"], events=[None]), lambda: stm.Mx4SparseMoE(p, dev, overlap_shared=True),
+            lambda: stm.Mx4SparseMoE(p, {**dev, "down": dev["gate_up"]}),
+            lambda: stm.Mx4SparseMoE(p, {**dev, "down": moe.w["gate_up"]}),
+            lambda: stm.Mx4SparseMoE(p, {**dev, "bias": None}),
+            lambda: stm.Mx4SparseMoE(p, {**dev, "gate_w": dev["gate_w"].cpu()})]
     for i, call in enumerate(bad):
         with pytest.raises(ValueError):
             call()

@@ -121,6 +121,17 @@ def test_unpermute_and_its_gradient(shape, dtype, y_dtype, empty):
     assert torch.equal(dy1.cpu(), ref1) and torch.equal(dw1, dw)
 
 
+# each number of slots, with enough tokens for several vectors a thread, widths that leave some of them without one,
+# and a width below them
+@pytest.mark.parametrize("dtype,y_dtype", TYPES)
+@pytest.mark.parametrize("shape", [(2400, 2056, 8, 1), (1200, 2056, 8, 2), (1200, 2056, 8, 3), (600, 2056, 8, 4),
+                                   (600, 2056, 8, 5), (600, 2056, 8, 6), (600, 2056, 8, 7), (600, 2056, 8, 8),
+                                   (600, 2056, 16, 9), (130000, 40, 4, 1)])
+def test_every_number_of_slots(shape, dtype, y_dtype):
+    test_unpermute_and_its_gradient(shape, dtype, y_dtype, 0.3)
+    test_permute_and_its_gradient(shape, dtype, 0.3)
+
+
 def test_infinite_and_nan_rows_stay_in_their_token():
     p = _problem((40, 64, 8, 2))
     sel, plan = _plan(p, 0.0)
@@ -263,6 +274,49 @@ def test_captured_and_on_a_stream_of_its_own():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+def test_a_training_step_captured_with_its_backward():
+    p = _problem((300, 512, 16, 4))
+    _, plan = _plan(p, 0.1)
+    x = _rand((p.T, p.H), torch.bfloat16, 1).cuda().requires_grad_(True)
+    w = torch.rand(p.T, p.k, device="cuda", requires_grad=True)
+    dout = _rand((p.T, p.H), torch.bfloat16, 2).cuda()
+
+    def step():
+        out = stm.unpermute_rows(p, stm.permute_rows(p, x, plan) * 2, plan, w)
+        return (out.detach(), *torch.autograd.grad(out, (x, w), dout))
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        held = step()
+    for seed in (3, 4):
+        with torch.no_grad():
+            x.copy_(_rand((p.T, p.H), torch.bfloat16, seed))
+            dout.copy_(_rand((p.T, p.H), torch.bfloat16, seed + 9))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, step()))
+
+
+def test_gradients_of_outputs_that_are_views():
+    """An expanded or transposed gradient of the output reaches the kernels whole."""
+    p = _problem((16, 16, 4, 2))
+    _, plan = _plan(p, 0.0)
+    w = torch.rand(p.T, p.k, device="cuda")
+    for pick in (lambda o: o.sum(), lambda o: (o.t() * torch.arange(256, device="cuda").view(16, 16).bfloat16()).sum()):
+        x = _rand((p.T, p.H), torch.bfloat16, 1).cuda().requires_grad_(True)
+        out = stm.unpermute_rows(p, stm.permute_rows(p, x, plan), plan, w)
+        out.retain_grad()
+        pick(out).backward()
+        dy, _ = stm.unpermute_rows_backward(p, out.grad.contiguous(), torch.zeros_like(stm.permute_rows(p, x.detach(), plan)),
+                                            plan, w)
+        assert torch.equal(x.grad, stm.permute_rows_backward(p, dy, plan))
 
 
 def test_refusals():
