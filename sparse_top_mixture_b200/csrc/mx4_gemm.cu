@@ -234,20 +234,15 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
 // operand bytes of its tiles (8 KB a unit and step, 4 KB for each 32 rows of A
 // that the average tile has). Few row tiles take narrow tiles, so that every
 // SM streams weights; many take wide ones, which re-read A least.
+// Called by a whole warp: a lane weighs one choice.
 __device__ __forceinline__ int choose_units(int row_tiles, int rows, int n_units, int grid) {
+  const int u = MAX_UNITS - min((int)(threadIdx.x & 31), MAX_UNITS - 1);
   const int boxes = row_tiles > 0 ? min(4, (rows / row_tiles + 31) / 32) : 1;
-  int best = MAX_UNITS;
-  uint32_t least = 0xffffffffu;
-#pragma unroll
-  for (int u = MAX_UNITS; u >= 1; --u) {
-    const uint32_t tiles = (uint32_t)row_tiles * ((uint32_t)(n_units + u - 1) / u);
-    const uint32_t cost = (tiles + grid - 1) / (uint32_t)grid * (2 * u + max(1, boxes));
-    if (cost < least) {
-      least = cost;
-      best = u;
-    }
-  }
-  return best;
+  const uint32_t tiles = (uint32_t)row_tiles * ((uint32_t)(n_units + u - 1) / u);
+  const uint32_t cost = (tiles + grid - 1) / (uint32_t)grid * (2 * u + max(1, boxes));
+  // the least cost, and of equal ones the most units
+  const uint32_t least = __reduce_min_sync(0xffffffffu, cost);
+  return MAX_UNITS - (__ffs(__ballot_sync(0xffffffffu, cost == least)) - 1);
 }
 
 struct Tile {
@@ -258,11 +253,19 @@ struct Tile {
 // segment); e is the expert of an earlier tile of the same CTA (row
 // tiles come in rising order).
 template <bool PAIR>
-__device__ __forceinline__ Tile decode(const Ctl* ctl, int units, int n_tiles, int tile, int e, int rank) {
+__device__ __forceinline__ Tile decode(const Ctl* ctl, int E, int units, int n_tiles, int tile, int e, int rank) {
   Tile t;
   const int mt = tile / n_tiles;
   t.unit0 = (tile - mt * n_tiles) * units;
-  while (ctl->pre[e + 1] <= mt) ++e;
+  if (ctl->pre[e + 1] <= mt) {  // pre[lo] <= mt < pre[hi]
+    int lo = e + 1, hi = E;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (ctl->pre[mid] <= mt) lo = mid;
+      else hi = mid;
+    }
+    e = lo;
+  }
   t.e = e;
   t.row0 = ctl->off[e] + (mt - ctl->pre[e]) * (PAIR ? 2 * BM : BM) + rank * BM;
   t.row_end = ctl->off[e + 1];
@@ -366,11 +369,10 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
   if (warp == SF_WARP0) {
     warp_build_tile_table(args.offsets, args.E, 0, PAIR ? 2 * BM : BM, ctl->off, ctl->pre, args.rows_total, args.err);
     __syncwarp();
-    if (lane == 0) {
+    if constexpr (!PAIR) {
       const int row_tiles = ctl->pre[args.E];
-      ctl->units = PAIR ? MAX_UNITS
-                        : choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units,
-                                       workers);
+      const int units = choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units, workers);
+      if (lane == 0) ctl->units = units;
     }
   }
   if (warp == 1) {
@@ -397,7 +399,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       const CUtensorMap* tmB = &maps.b[PAIR ? 0 : units - 1];
       bool seen = false;
       for (int tile = worker; ok && tile < total; tile += workers) {
-        const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
+        const Tile t = decode<PAIR>(ctl, args.E, units, n_tiles, tile, e, rank);
         e = t.e;
         // boxes of A that the rows from row0 on fill, and their bytes
         auto boxes_from = [&](int row0) {
@@ -572,7 +574,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       if (tile >= total) break;
       if (set_up) {
         set_up = false;
-        const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
+        const Tile t = decode<PAIR>(ctl, args.E, units, n_tiles, tile, e, rank);
         e = t.e;
 #pragma unroll
         for (int c = 0; c < kA; ++c) {
@@ -642,7 +644,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     int e = 0;
     [[maybe_unused]] int other = 0;
     for (int tile = worker + acc * workers; tile < total; tile += 2 * workers) {
-      const Tile t = decode<PAIR>(ctl, units, n_tiles, tile, e, rank);
+      const Tile t = decode<PAIR>(ctl, args.E, units, n_tiles, tile, e, rank);
       e = t.e;
       const int row_w0 = t.row0 + quarter * 32;
       const int nrows = t.row_end - row_w0;
@@ -780,7 +782,7 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
   if (e != cudaSuccess) return e;
   if (!get_encode()) return cudaErrorNotSupported;
   Maps maps;
-  for (int i = 0; i < 2; ++i) {
+  for (int i = 0; i < (rows > BM - A_BOX_ROWS ? 2 : 1); ++i) {  // fewer rows never fill the tile's box
     const uint64_t dims[2] = {(uint64_t)K / 2, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)K / 2};
     const uint32_t box[2] = {BK / 2, (uint32_t)(i == 0 ? A_BOX_ROWS : BM)};

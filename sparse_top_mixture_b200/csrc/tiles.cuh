@@ -31,15 +31,18 @@ __device__ __forceinline__ void warp_build_tile_table(const int32_t* __restrict_
     }
     return;
   }
-  int c[8];
+  int c[8], bound[9];
   int local = 0;
   bool bad = false;
+  // every load before the first use: behind the conditions below they would wait for one another
+#pragma unroll
+  for (int i = 0; i <= 8; ++i) bound[i] = offsets[min(lane * 8 + i, E)];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int e = lane * 8 + i;
     c[i] = 0;
     if (e < E) {
-      const int a = offsets[e], b = offsets[e + 1];
+      const int a = bound[i], b = bound[i + 1];
       bad |= a < 0 || b < a || (int64_t)b > rows_total;
       off[e] = a;
       c[i] = (b - a + BM - 1) / BM;

@@ -18,8 +18,7 @@ takes part in autograd.
 
 from __future__ import annotations
 
-from dataclasses import dataclass
-from typing import Dict, Optional, Sequence, Tuple
+from typing import Dict, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
@@ -29,8 +28,7 @@ from .rows import _plan, _same_device
 _DTYPE_ID = {TORCH_DTYPE[name]: i for name, i in DTYPES.items()}
 
 
-@dataclass(frozen=True)
-class Mx4:
+class Mx4(NamedTuple):
     """Rows of 4-bit values: ``data`` uint8 [..., K/2], ``scale`` uint8 [..., 16*ceil(K/512)]."""
 
     data: torch.Tensor
@@ -65,16 +63,20 @@ def _req_mx4(q: Mx4, name: str, lead: Optional[Sequence[int]] = None) -> int:
     """K of q, which has leading dimensions `lead` (None: any)."""
     if not isinstance(q, Mx4):
         raise ValueError(f"{name} must be an Mx4")
-    if not isinstance(q.data, torch.Tensor) or q.data.dim() < 1:
+    data, scale = q
+    if not isinstance(data, torch.Tensor) or data.dim() < 1:
         raise ValueError(f"{name}.data must be a CUDA tensor of at least one dimension")
-    shape = q.data.shape
+    shape = data.shape
     K = 2 * shape[-1]
-    _req_k(K, name)
-    lead = tuple(shape[:-1] if lead is None else lead)
-    _req(q.data, f"{name}.data", lead + (K // 2,), torch.uint8)
-    _req(q.scale, f"{name}.scale", lead + (_scale_bytes(K),), torch.uint8)
-    if q.scale.get_device() != q.data.get_device():
-        raise ValueError(f"{name}.scale is on {q.scale.device}, expected {q.data.device}")
+    lead = shape[:-1] if lead is None else tuple(lead)
+    if not (K > 0 and K % 32 == 0 and data.is_cuda and data.dtype == torch.uint8 and data.is_contiguous()
+            and shape[:-1] == lead and isinstance(scale, torch.Tensor) and scale.get_device() == data.get_device()
+            and scale.dtype == torch.uint8 and scale.is_contiguous()
+            and scale.shape == lead + (16 * -(-K // 512),)):  # which of it, in words:
+        _req_k(K, name)
+        _req(data, f"{name}.data", lead + (K // 2,), torch.uint8)
+        _req(scale, f"{name}.scale", lead + (_scale_bytes(K),), torch.uint8)
+        raise ValueError(f"{name}.scale is on {scale.device}, expected {data.device}")
     return K
 
 
