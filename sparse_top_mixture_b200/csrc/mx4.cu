@@ -213,8 +213,8 @@ MOE_API moe_status moe_mx4_dequantize(int64_t rows, int64_t K, int32_t dtype, co
   const uint32_t* d = static_cast<const uint32_t*>(data);
   const uint8_t* sc = static_cast<const uint8_t*>(scale);
   if (dtype == MOE_DTYPE_F32)
-    dequantize_kernel<float><<<warp_grid(rows * chunks, kManyBlocks), QTHREADS, 0, s>>>(d, sc, rows, (int)K, pitch, chunks,
-                                                                           static_cast<float*>(out));
+    dequantize_kernel<float><<<warp_grid(rows * chunks, kManyBlocks), QTHREADS, 0, s>>>(
+        d, sc, rows, (int)K, pitch, chunks, static_cast<float*>(out));
   else
     dequantize_kernel<__nv_bfloat16><<<warp_grid(rows * chunks, kManyBlocks), QTHREADS, 0, s>>>(
         d, sc, rows, (int)K, pitch, chunks, static_cast<__nv_bfloat16*>(out));

@@ -15,7 +15,7 @@
 // tensor cores (at N 192 and 256 values of K, 28 KB in and some 40 KB out a
 // step of 384 MMA clocks, 128 bytes a clock), and the power limit, which holds
 // the SM clock near 1.5 GHz (gate_up of 8192 tokens, 64 experts, H 4096, I 2048:
-// 409 us, 4.0 PFLOP/s).
+// 410 us, 4.0 PFLOP/s).
 //
 // Design (a CTA on each SM, persistent, warp-specialised, 480 threads):
 //   warp 0      TMA producer, 256 values of K a step: the tile's rows of A (one
@@ -23,8 +23,8 @@
 //               64 rows of W per unit of the tile; for gate_up 32 gate rows per
 //               unit and then the 32 up rows of the same features.
 //   warp 1      MMA issuer: up to four MMAs a step. Two accumulators.
-//   warp 2      copies the scales of two steps from shared memory to TMEM, into
-//               one of two sets of columns.
+//   warp 2      copies each step's scales from shared memory to TMEM, into the
+//               columns of the step's stage.
 //   warps 3-6   scale producers: the tensor core wants the four scale bytes of
 //               a row's 128 values as one word, row r at lane r % 32 and column
 //               r / 32. A lane loads 16 scale bytes (512 values) of its rows r,
@@ -67,11 +67,9 @@ constexpr int UNIT_BYTES = UNIT * BK / 2;
 constexpr int SF_ATOM_BYTES = 512;   // scale words of 128 rows for 128 values of K; a vector has four
 constexpr int MAX_STAGES = 8;
 constexpr int ACC_COLS = MAX_UNITS * UNIT;         // TMEM columns of one accumulator
-constexpr int SF_COL = 2 * ACC_COLS;               // two sets of scale columns follow
-constexpr int SFB_COL = 4 * 4;                     // in a set: four atoms of A, then four of B (up to 256 rows)
-constexpr int SF_SET_COLS = SFB_COL + 4 * 8;
+constexpr int SF_COL = 2 * ACC_COLS;               // the stages' scale columns follow: two atoms of A, two of B
+constexpr int SFB_COL = 2 * 4;
 constexpr int TMEM_COLS = 512;
-static_assert(SF_COL + 2 * SF_SET_COLS <= TMEM_COLS, "accumulators and scales fit TMEM");
 constexpr int SF_STAGES = 4;                       // one for each scale warp
 constexpr int SF_WARP0 = 3;
 constexpr int EPI_WARP0 = SF_WARP0 + SF_STAGES;
@@ -87,6 +85,11 @@ __host__ __device__ constexpr int ring_stages(int units, bool pair) {
   return RING_BYTES / stage_bytes(units, pair) < MAX_STAGES ? RING_BYTES / stage_bytes(units, pair) : MAX_STAGES;
 }
 __host__ __device__ constexpr int sfb_blocks(int units) { return (units * UNIT + 127) / 128; }
+__host__ __device__ constexpr int sf_cols(int units) { return SFB_COL + 2 * 4 * sfb_blocks(units); }
+static_assert(SF_COL + ring_stages(1, false) * sf_cols(1) <= TMEM_COLS, "accumulators and scales fit TMEM");
+static_assert(SF_COL + ring_stages(2, false) * sf_cols(2) <= TMEM_COLS, "accumulators and scales fit TMEM");
+static_assert(SF_COL + ring_stages(3, false) * sf_cols(3) <= TMEM_COLS, "accumulators and scales fit TMEM");
+static_assert(SF_COL + ring_stages(3, true) * sf_cols(3) <= TMEM_COLS, "accumulators and scales fit TMEM");
 __host__ __device__ constexpr int sf_stage_bytes(int units) { return 4 * (1 + sfb_blocks(units)) * SF_ATOM_BYTES; }
 constexpr int SF_RING_BYTES = SF_STAGES * sf_stage_bytes(3);
 
@@ -122,8 +125,6 @@ struct __align__(8) Ctl {
   uint64_t empty[MAX_STAGES];
   uint64_t sfull[SF_STAGES];
   uint64_t sempty[SF_STAGES];
-  uint64_t cfull[2];   // a set of scale columns is filled, and free again
-  uint64_t cempty[2];
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;   // every MMA is done, and every copy of scales
@@ -170,14 +171,16 @@ __device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t b
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+            d),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   else
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
+            d),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
@@ -348,7 +351,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < MAX_STAGES; ++s) {
-      mbar_init(&ctl->full[s], 1);
+      mbar_init(&ctl->full[s], 2);  // the TMA producer and the scale copier
       mbar_init(&ctl->empty[s], 1);
     }
     for (int s = 0; s < SF_STAGES; ++s) {
@@ -356,8 +359,6 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       mbar_init(&ctl->sempty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
-      mbar_init(&ctl->cfull[a], 1);
-      mbar_init(&ctl->cempty[a], 1);
       mbar_init(&ctl->tfull[a], 1);
       mbar_init(&ctl->tempty[a], PAIR ? 8 : 4);  // the accumulator's epilogue warps
     }
@@ -371,7 +372,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     __syncwarp();
     if constexpr (!PAIR) {
       const int row_tiles = ctl->pre[args.E];
-      const int units = choose_units(row_tiles, row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0, args.n_units, workers);
+      const int rows = row_tiles > 0 ? ctl->off[args.E] - ctl->off[0] : 0;
+      const int units = choose_units(row_tiles, rows, args.n_units, workers);
       if (lane == 0) ctl->units = units;
     }
   }
@@ -453,7 +455,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       // Every copy has landed before the CTA may exit (a pair's leader counts
       // both CTAs' bytes, and the CTAs exit together).
       for (int s = 0; s < stages; ++s)
-        if (leader && ((issued >> s) & 1u)) mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
+        if (leader && ((issued >> s) & 1u))
+          mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -464,18 +467,14 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       constexpr int M = PAIR ? 2 * BM : BM;
       const uint32_t idesc0 = make_idesc_mxf4(M, units * UNIT, 0), idesc2 = make_idesc_mxf4(M, units * UNIT, 2);
       const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
-      int stage = 0, acc = 0, set = 0;
-      uint32_t phase = 0, set_phase = 0, acc_phase = 0;
-      bool ok = true, seen = false, set_seen = false;
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true, seen = false;
       for (int tile = worker; ok && tile < total; tile += workers) {
         if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
         for (int kt = 0; kt < args.k_steps; ++kt) {
-          if ((kt & 1) == 0 && !set_seen && !mbar_wait(&ctl->cfull[set], set_phase, &ctl->abort, args.err, 8)) {
-            ok = false;
-            break;
-          }
           if (!seen && !mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
             ok = false;
             break;
@@ -485,24 +484,17 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
           const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
           seen = mbar_test(&ctl->full[next], next_phase);
           const uint32_t sa = smem_base + stage * sbytes;
-          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS + (kt & 1) * 8;
-          const uint32_t sfb = tmem_base + SF_COL + set * SF_SET_COLS + SFB_COL + (kt & 1) * 16;
+          const uint32_t sfa = tmem_base + SF_COL + stage * sf_cols(units), sfb = sfa + SFB_COL;
           const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
           const bool last = kt + 1 == args.k_steps;
           const int left = last ? k_tail : BK;
           umma_mxf4<PAIR>(d_tmem, adesc, bdesc, idesc0, sfa, sfb, kt > 0 ? 1u : 0u);
           if (left > 64) umma_mxf4<PAIR>(d_tmem, adesc + 2, bdesc + 2, idesc2, sfa, sfb, 1u);
-          if (left > 128) umma_mxf4<PAIR>(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 8, 1u);
-          if (left > 192) umma_mxf4<PAIR>(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 8, 1u);
+          if (left > 128) umma_mxf4<PAIR>(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 4 * blocks, 1u);
+          if (left > 192) umma_mxf4<PAIR>(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 4 * blocks, 1u);
           commit<PAIR>(&ctl->empty[stage]);
           stage = next;
           phase = next_phase;
-          if ((kt & 1) || last) {
-            commit_here<PAIR>(&ctl->cempty[set]);
-            set ^= 1;
-            if (set == 0) set_phase ^= 1u;
-            set_seen = mbar_test(&ctl->cfull[set], set_phase);
-          }
         }
         if (!ok) break;
         commit<PAIR>(&ctl->tfull[acc]);
@@ -517,37 +509,42 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
   } else if (warp == 2) {
     // ---------------- scales from shared memory to TMEM ----------------
     // A thread of its own: twelve copies for every two steps took a third of the
-    // MMA issuer's time (420 us a gate_up that now takes 409).
+    // MMA issuer's time. Every stage of the operands has its columns, so that a
+    // step's copies complete its full barrier like its operands.
     if (leader && elect_one()) {
-      const int sf_bytes = sf_stage_bytes(units), n_vec = (args.k_steps + 1) / 2;
+      const int stages = ring_stages(units, PAIR), sf_bytes = sf_stage_bytes(units);
       const uint32_t sf_smem = smem_u32(sf_base);
-      int sf_stage = 0, set = 0;
-      uint32_t sf_phase = 0, set_phase = 0;
+      int stage = 0, sf_stage = 0;
+      uint32_t phase = 0, sf_phase = 0;
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += workers) {
-        for (int kv = 0; kv < n_vec; ++kv) {
-          ok = mbar_wait(&ctl->cempty[set], set_phase ^ 1u, &ctl->abort, args.err, 9) &&
-               mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 10);
+        for (int kt = 0; kt < args.k_steps; ++kt) {
+          ok = mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 9) &&
+               ((kt & 1) || mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 10));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sfa = tmem_base + SF_COL + set * SF_SET_COLS, sfb = sfa + SFB_COL;
-          const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes), db = da + 4 * (SF_ATOM_BYTES / 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) copy_scales<PAIR>(sfa + 4 * i, da + i * (SF_ATOM_BYTES / 16));
-          if (blocks == 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) copy_scales<PAIR>(sfb + 8 * i, db + i * (SF_ATOM_BYTES / 16));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) copy_scales<PAIR>(sfb + 4 * i, db + i * (SF_ATOM_BYTES / 16));
+          const uint32_t sfa = tmem_base + SF_COL + stage * sf_cols(units), sfb = sfa + SFB_COL;
+          const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes + (kt & 1) * 2 * SF_ATOM_BYTES);
+          const uint64_t db = sf_desc(sf_smem + sf_stage * sf_bytes + (4 + (kt & 1) * 2 * blocks) * SF_ATOM_BYTES);
+          copy_scales<PAIR>(sfa, da);
+          copy_scales<PAIR>(sfa + 4, da + SF_ATOM_BYTES / 16);
+          copy_scales<PAIR>(sfb, db);
+          copy_scales<PAIR>(sfb + 4, db + SF_ATOM_BYTES / 16);
+          if (blocks == 2) {
+            copy_scales<PAIR>(sfb + 8, db + 2 * (SF_ATOM_BYTES / 16));
+            copy_scales<PAIR>(sfb + 12, db + 3 * (SF_ATOM_BYTES / 16));
           }
-          commit_here<PAIR>(&ctl->cfull[set]);
-          commit<PAIR>(&ctl->sempty[sf_stage]);
-          set ^= 1;
-          if (set == 0) set_phase ^= 1u;
-          if (++sf_stage == SF_STAGES) {
-            sf_stage = 0;
-            sf_phase ^= 1u;
+          commit_here<PAIR>(&ctl->full[stage]);
+          if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if ((kt & 1) || kt + 1 == args.k_steps) {
+            commit<PAIR>(&ctl->sempty[sf_stage]);
+            if (++sf_stage == SF_STAGES) {
+              sf_stage = 0;
+              sf_phase ^= 1u;
+            }
           }
         }
       }
@@ -579,7 +576,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
 #pragma unroll
         for (int c = 0; c < kA; ++c) {
           const int row = t.row0 + 32 * c + lane;
-          src_a[c] = row < t.row_end ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch) : nullptr;
+          src_a[c] = row < t.row_end ? reinterpret_cast<const uint4*>(args.a_scale + (int64_t)row * args.pitch)
+                                     : nullptr;
         }
         const uint8_t* w = args.b_scale + (int64_t)e * args.b_rows * args.pitch;
 #pragma unroll
@@ -602,13 +600,17 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
         // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
         const int valid = args.K / mx4::kBlock - kv * 16 - atom * 4;
         const uint32_t mask = valid >= 4 ? 0xffffffffu : valid <= 0 ? 0u : (1u << (8 * valid)) - 1u;
-        auto word = [&](const uint4& v) { return mask & (atom == 0 ? v.x : atom == 1 ? v.y : atom == 2 ? v.z : v.w); };
-        *reinterpret_cast<uint4*>(stage_base + atom * SF_ATOM_BYTES) = make_uint4(word(va[0]), word(va[1]), word(va[2]), word(va[3]));
+        auto word = [&](const uint4& v) {
+          return mask & (atom == 0 ? v.x : atom == 1 ? v.y : atom == 2 ? v.z : v.w);
+        };
+        *reinterpret_cast<uint4*>(stage_base + atom * SF_ATOM_BYTES) =
+            make_uint4(word(va[0]), word(va[1]), word(va[2]), word(va[3]));
         const uint4 lo = make_uint4(word(vb[0]), word(vb[1]), word(vb[2]), word(vb[3]));
         uint8_t* dst_b = stage_base + 4 * SF_ATOM_BYTES;
         if (blocks == 2) {
           *reinterpret_cast<uint4*>(dst_b + 2 * atom * SF_ATOM_BYTES) = lo;
-          *reinterpret_cast<uint4*>(dst_b + (2 * atom + 1) * SF_ATOM_BYTES) = make_uint4(word(vb[4]), word(vb[5]), 0u, 0u);
+          *reinterpret_cast<uint4*>(dst_b + (2 * atom + 1) * SF_ATOM_BYTES) =
+              make_uint4(word(vb[4]), word(vb[5]), 0u, 0u);
         } else {
           *reinterpret_cast<uint4*>(dst_b + atom * SF_ATOM_BYTES) = lo;
         }
@@ -797,14 +799,17 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
     const uint64_t strides[3] = {(uint64_t)K / 2, (uint64_t)N * K / 2, halves * (uint64_t)N * K / 2};
     const uint32_t box[4] = {BK / 2, PAIR ? MAX_UNITS * UNIT / 2u : (uint32_t)(u * UNIT / halves),
                              PAIR ? 1u : (uint32_t)halves, 1};
-    if (!make_tensor_map(&maps.b[u - 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, w_data, 4, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!make_tensor_map(&maps.b[u - 1], CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, w_data, 4, dims,
+                         strides, box))
+      return cudaErrorInvalidValue;
   }
   if (MODE != SWIGLU_MX4) {
     const uint64_t es = MODE == OUT_F32 ? 4 : 2;
     const uint64_t dims[2] = {(uint64_t)N, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)N * es};
     const uint32_t box[2] = {MODE == OUT_BF16 ? 64u : 32u, 32};
-    if (!make_tensor_map(&maps.out, MODE == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+    if (!make_tensor_map(&maps.out,
+                         MODE == OUT_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                          MODE == SWIGLU_BF16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, out, 2, dims,
                          strides, box))
       return cudaErrorInvalidValue;
@@ -835,8 +840,8 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
 
 // Pairs halve the traffic of W but fill 256-row tiles: they pay from about 512
 // rows an expert on (us, one CTA / pairs: 64 experts of N 4096, K 2048 at 256
-// rows each 105 / 104, at 512 171 / 165, at 1536 443 / 407; 128 experts of N
-// 2048, K 768 at 256 58 / 60, at 1536 242 / 227), and lose with few steps a
+// rows each 105 / 104, at 512 170 / 165, at 1536 435 / 399; 128 experts of N
+// 2048, K 768 at 256 58 / 60, at 1536 244 / 231), and lose with few steps a
 // pair (gate_up of 16 experts, H 1024, I 512 at 768: 23.6 / 25.3).
 bool use_pairs(int64_t rows, int64_t E, int64_t n_units, int64_t k_steps) {
   return rows >= 512 * E && rows / (2 * BM) * ceil_div(n_units, MAX_UNITS) * k_steps >= 64 * (num_sms() / 2);

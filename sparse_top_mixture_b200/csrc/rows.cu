@@ -399,8 +399,8 @@ cudaError_t launch_unpermute(const void* ys, const int32_t* pair_pos, const floa
     auto launch = [&](auto kernel, int per_thread) {
       const int64_t passes = ceil_div(nvec, per_thread);
       const int lg = lane_log2(passes);
-      kernel<<<lane_grid(T, passes, lg, kResident), RTHREADS, 0, s>>>(static_cast<const TY*>(ys), pair_pos, w, shared_out,
-                                                          static_cast<TO*>(out), T, (int)H, (int)k, lg);
+      kernel<<<lane_grid(T, passes, lg, kResident), RTHREADS, 0, s>>>(
+          static_cast<const TY*>(ys), pair_pos, w, shared_out, static_cast<TO*>(out), T, (int)H, (int)k, lg);
     };
     if (many(T, nvec, V)) launch(unpermute_rows_kernel<TY, TO, SL, V>, V);
     else launch(unpermute_rows_kernel<TY, TO, SL, 1>, 1);
@@ -452,7 +452,8 @@ MOE_API moe_status moe_permute_rows(const moe_problem* p, const void* x, const i
     // Blocks that end early are replaced as they end, which evens out the stores
     // (8192 x 2048 bf16, k 8: 54 us with resident blocks, 49 so); with k 1 there
     // is nothing to even out (20.7 and 22.7 us of 8192 x 4096).
-    kernel<<<lane_grid(p->T, passes, lg, p->k == 1 ? kResident : kResident * 64), RTHREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+    const dim3 grid = lane_grid(p->T, passes, lg, p->k == 1 ? kResident : kResident * 64);
+    kernel<<<grid, RTHREADS, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
         static_cast<const uint4*>(x), pair_pos, offsets, static_cast<uint4*>(x_perm), p->T, (int)nvec, (int)p->k,
         (int)p->E, lg);
   };
