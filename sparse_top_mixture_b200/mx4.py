@@ -23,7 +23,7 @@ from typing import Dict, NamedTuple, Optional, Sequence, Tuple
 import torch
 
 from . import DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, lib, new_workspace
-from .rows import _plan, _same_device
+from .rows import _plan, _req_at
 
 _DTYPE_ID = {TORCH_DTYPE[name]: i for name, i in DTYPES.items()}
 
@@ -119,9 +119,8 @@ def mx4_permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]) -> Mx4:
     [T*k, H] in 4 bits, sorted by expert; rows past the last segment are zeros."""
     _req(x, "x", (p.T, p.H), TORCH_DTYPE[p.dtype])
     _req_k(p.H, "x")
-    pair_pos, offsets = _plan(p, plan)
     dev = x.device
-    _same_device(dev, pair_pos=pair_pos, offsets=offsets)
+    pair_pos, offsets = _plan(p, plan, dev.index)
     q = _new((p.T * p.k,), p.H, dev)
     _launch(lib().moe_mx4_permute_rows, dev, p.c(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(),
             q.data.data_ptr(), q.scale.data_ptr())
@@ -135,10 +134,13 @@ def _req_product(a: Mx4, w: Mx4, offsets, ws) -> int:
         raise ValueError(f"a has K {K}, w {w.K}")
     if a.data.dim() != 2 or w.data.dim() != 3:
         raise ValueError("a must be [rows, K] and w [E, N, K]")
-    _req(offsets, "offsets", (w.data.shape[0] + 1,), torch.int32)
-    if ws is not None and (not isinstance(ws, torch.Tensor) or not ws.is_cuda or ws.numel() * ws.element_size() < 256):
-        raise ValueError("ws must be a workspace")
-    _same_device(a.data.device, w=w.data, offsets=offsets, ws=ws)
+    index = a.data.get_device()
+    _req_at(offsets, "offsets", (w.data.shape[0] + 1,), torch.int32, index)
+    if w.data.get_device() != index:
+        raise ValueError(f"w is on {w.device}, expected cuda:{index}")
+    if ws is not None and (not isinstance(ws, torch.Tensor) or ws.get_device() != index
+                           or ws.numel() * ws.element_size() < 256):
+        raise ValueError(f"ws must be a workspace on cuda:{index}")
     return K
 
 
@@ -216,9 +218,10 @@ class Mx4SparseMoE(SparseMoE):
         self.ws = new_workspace(p, self.device)
         self.aux = None
         self._counts = torch.zeros(p.E, dtype=torch.int32, device=self.device)
-        experts = {name: w[name].data for name in ("gate_up", "down")}
-        others = {name: w.get(name) for name in ("gate_w", "bias", "shared_gate", "shared_gate_up", "shared_down")}
-        _same_device(self.ws.device, **experts, **others)
+        on = [w["gate_up"].data, w["down"].data] + [w.get(name) for name in ("gate_w", "bias", "shared_gate",
+                                                                             "shared_gate_up", "shared_down")]
+        if any(t is not None and t.device != self.ws.device for t in on):
+            raise ValueError(f"the weights must be on {self.ws.device}")
 
     def forward(self, x, out=None, routing_weights=None, selected_experts=None, events=None):
         """out, routing_weights, selected_experts = moe(x), as SparseMoE's."""
@@ -226,11 +229,11 @@ class Mx4SparseMoE(SparseMoE):
             raise ValueError("stage events are recorded by SparseMoE only")
         p, w, ws = self.p, self.w, self.ws
         out, rw, sel = self._outputs(x, out, routing_weights, selected_experts)
-        _req(out, "out", (p.T, p.H), torch.bfloat16)
-        _req(rw, "routing_weights", (p.T, p.k), torch.float32)
-        _req(sel, "selected_experts", (p.T, p.k), torch.int64)
         dev = ws.device
-        _same_device(dev, x=x, out=out, routing_weights=rw, selected_experts=sel)
+        _req_at(x, "x", (p.T, p.H), torch.bfloat16, dev.index)
+        _req_at(out, "out", (p.T, p.H), torch.bfloat16, dev.index)
+        _req_at(rw, "routing_weights", (p.T, p.k), torch.float32, dev.index)
+        _req_at(sel, "selected_experts", (p.T, p.k), torch.int64, dev.index)
         gate = w.get("shared_gate")
         gamma = None if gate is None else torch.empty(p.T, dtype=torch.float32, device=dev)
         _launch(lib().moe_route, dev, p.c(), x.data_ptr(), w["gate_w"].data_ptr(), _ptr(w.get("bias")), _ptr(gate),

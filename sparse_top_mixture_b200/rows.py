@@ -29,18 +29,20 @@ import torch
 from . import DTYPES, TORCH_DTYPE, Problem, _launch, _ptr, _req, lib
 
 
-def _plan(p: Problem, plan: Dict[str, torch.Tensor]) -> Tuple[torch.Tensor, torch.Tensor]:
+def _req_at(t, name: str, shape: Tuple[int, ...], dtype: torch.dtype, index: int) -> None:
+    """_req, on the CUDA device of that index."""
+    if (isinstance(t, torch.Tensor) and t.get_device() == index and t.dtype == dtype and t.shape == shape
+            and t.is_contiguous()):
+        return
+    _req(t, name, shape, dtype)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
+
+
+def _plan(p: Problem, plan: Dict[str, torch.Tensor], index: int) -> Tuple[torch.Tensor, torch.Tensor]:
     pair_pos, offsets = plan["pair_pos"], plan["offsets"]
-    _req(pair_pos, "pair_pos", (p.T * p.k,), torch.int32)
-    _req(offsets, "offsets", (p.E + 1,), torch.int32)
+    _req_at(pair_pos, "pair_pos", (p.T * p.k,), torch.int32, index)
+    _req_at(offsets, "offsets", (p.E + 1,), torch.int32, index)
     return pair_pos, offsets
-
-
-def _same_device(dev: torch.device, **tensors: Optional[torch.Tensor]) -> None:
-    index = dev.index
-    for name, t in tensors.items():
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
 
 
 def _req_y(p: Problem, y_perm) -> int:
@@ -122,8 +124,7 @@ def permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]):
     """x_perm [T*k, H]: each token's row of x [T, H] copied to its k sorted
     positions. Rows past the last segment are zeros. Differentiable in x."""
     _req(x, "x", (p.T, p.H), TORCH_DTYPE[p.dtype])
-    pair_pos, offsets = _plan(p, plan)
-    _same_device(x.device, pair_pos=pair_pos, offsets=offsets)
+    pair_pos, offsets = _plan(p, plan, x.get_device())
     if x.requires_grad and torch.is_grad_enabled():
         return _PermuteRows.apply(x, p, pair_pos, offsets)
     return _permute(p, x, pair_pos, offsets)
@@ -133,8 +134,7 @@ def permute_rows_backward(p: Problem, dx_perm, plan: Dict[str, torch.Tensor]):
     """dx [T, H] from dx_perm [T*k, H] (both in the problem's dtype): the sum
     of each token's k rows, in fp32, rounded once."""
     _req(dx_perm, "dx_perm", (p.T * p.k, p.H), TORCH_DTYPE[p.dtype])
-    pair_pos, _ = _plan(p, plan)
-    _same_device(dx_perm.device, pair_pos=pair_pos)
+    pair_pos, _ = _plan(p, plan, dx_perm.get_device())
     return _permute_backward(p, dx_perm, pair_pos)
 
 
@@ -145,15 +145,16 @@ def unpermute_rows(p: Problem, y_perm, plan: Dict[str, torch.Tensor], routing_we
     once to the problem's dtype. A slot without a row adds nothing.
     Differentiable in y_perm, routing_weights and shared_out."""
     yd = _req_y(p, y_perm)
-    pair_pos, offsets = _plan(p, plan)
+    index = y_perm.get_device()
+    pair_pos, offsets = _plan(p, plan, index)
+    grad = y_perm.requires_grad
     if routing_weights is not None:
-        _req(routing_weights, "routing_weights", (p.T, p.k), torch.float32)
+        _req_at(routing_weights, "routing_weights", (p.T, p.k), torch.float32, index)
+        grad = grad or routing_weights.requires_grad
     if shared_out is not None:
-        _req(shared_out, "shared_out", (p.T, p.H), torch.float32)
-    _same_device(y_perm.device, pair_pos=pair_pos, offsets=offsets, routing_weights=routing_weights,
-                 shared_out=shared_out)
-    if (y_perm.requires_grad or (routing_weights is not None and routing_weights.requires_grad)
-            or (shared_out is not None and shared_out.requires_grad)) and torch.is_grad_enabled():
+        _req_at(shared_out, "shared_out", (p.T, p.H), torch.float32, index)
+        grad = grad or shared_out.requires_grad
+    if grad and torch.is_grad_enabled():
         return _UnpermuteRows.apply(y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets)
     return _unpermute(p, yd, y_perm, pair_pos, routing_weights, shared_out)
 
@@ -163,10 +164,10 @@ def unpermute_rows_backward(p: Problem, dout, y_perm, plan: Dict[str, torch.Tens
     dout [T, H]: each row's gradient is its weight times dout (rows past the
     last segment are zeros), each weight's the product of dout and its row (0
     for a slot without a row)."""
-    _req(dout, "dout", (p.T, p.H), TORCH_DTYPE[p.dtype])
     yd = _req_y(p, y_perm)
-    pair_pos, offsets = _plan(p, plan)
+    index = y_perm.get_device()
+    _req_at(dout, "dout", (p.T, p.H), TORCH_DTYPE[p.dtype], index)
+    pair_pos, offsets = _plan(p, plan, index)
     if routing_weights is not None:
-        _req(routing_weights, "routing_weights", (p.T, p.k), torch.float32)
-    _same_device(dout.device, y_perm=y_perm, pair_pos=pair_pos, offsets=offsets, routing_weights=routing_weights)
+        _req_at(routing_weights, "routing_weights", (p.T, p.k), torch.float32, index)
     return _unpermute_backward(p, yd, dout, y_perm, pair_pos, offsets, routing_weights, True, True)
