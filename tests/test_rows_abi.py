@@ -55,3 +55,33 @@ def test_unpermute_rows_backward_validates():
            (A, A, A, None, A, A, A)]   # the rows' gradient needs the offsets
     for args in bad:
         assert L.moe_unpermute_rows_backward(_p(), 1, *args, None) == 1
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_a_launch_has_its_device_current_and_its_stream(monkeypatch, current):
+    """For tensors on another device than the current one (no GPU: the calls that would ask for one are stood in for)."""
+    import contextlib
+
+    import torch
+
+    state = {"device": current}
+
+    @contextlib.contextmanager
+    def device(d):
+        before, state["device"] = state["device"], d.index
+        yield
+        state["device"] = before
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda i: 100 + i, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    seen = []
+
+    def call(a, b, stream):
+        seen.append((a, b, stream, state["device"]))
+        return 0
+
+    stm._launch(call, torch.device("cuda", 1), 5, None)
+    assert seen == [(5, None, 101, 1)] and state["device"] == current
+    with pytest.raises(stm.MoeError):
+        stm._launch(lambda *a: 1, torch.device("cuda", 0))
