@@ -149,58 +149,140 @@ __device__ __forceinline__ uint32_t make_idesc_mxf4(int M, int N, uint32_t half)
          (half << 4) | (half << 29);
 }
 
-// Shared-memory descriptor of one scale atom for tcgen05.cp: 32 rows of 16
-// bytes, no swizzle, 8-row groups 128 bytes apart.
-__device__ __forceinline__ uint64_t sf_desc(uint32_t saddr) {
-  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
+// The three issuing threads (TMA, MMA, scale copies) each run one loop a step,
+// which has to stay below the step's 384 MMA clocks: they keep shared-memory
+// addresses as 32-bit words that a step advances, and descriptors as their low
+// words; the first two test the next step's barrier before the present step's
+// work (a wait takes about 100 clocks even when its phase is long complete). With
+// pointers, indices and whole descriptors gate_up of 8192 tokens took 412 us, so
+// 406.
+
+// High words of the descriptors: an operand (128-byte swizzle, 8-row groups
+// 1024 bytes apart, see sw128_desc), and a scale atom for tcgen05.cp (32 rows of
+// 16 bytes, no swizzle, 8-row groups 128 bytes apart). The low word is the
+// address / 16, with 1 in the leading offset.
+#define MX4_DESC_HIGH "0x40004040"
+#define MX4_SF_DESC_HIGH "0x00004008"
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) { return saddr >> 4 | 1u << 16; }
 
 // Of a pair, both CTAs copy from their own shared memory to their own TMEM.
 template <bool PAIR>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t sdesc) {
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint32_t desc) {
   if constexpr (PAIR)
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, " MX4_SF_DESC_HIGH "};\n\t"
+                 "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], d;\n\t}\n" ::"r"(taddr), "r"(desc) : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc) : "memory");
+    asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, " MX4_SF_DESC_HIGH "};\n\t"
+                 "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}\n" ::"r"(taddr), "r"(desc) : "memory");
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void umma_mxf4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+__device__ __forceinline__ void umma_mxf4(uint32_t d, uint32_t adesc, uint32_t bdesc, uint32_t idesc, uint32_t sfa,
                                           uint32_t sfb, uint32_t accumulate) {
   if constexpr (PAIR)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, " MX4_DESC_HIGH "};\n\tmov.b64 db, {%2, " MX4_DESC_HIGH "};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-            d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+        "mov.b64 da, {%1, " MX4_DESC_HIGH "};\n\tmov.b64 db, {%2, " MX4_DESC_HIGH "};\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(
-            d),
-        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+        "r"(adesc), "r"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
 
-// Arrive on `bar` once the work that this thread has issued so far is done;
-// commit: of a pair, in both CTAs.
+// Arrive on the barrier at `bar`, a pair's in both CTAs, once the work that this
+// thread has issued so far is done; commit_here: on this CTA's only.
 template <bool PAIR>
-__device__ __forceinline__ void commit_here(uint64_t* bar) {
+__device__ __forceinline__ void commit_here(uint32_t bar) {
   if constexpr (PAIR)
-    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
   else
-    umma_commit(bar);
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 template <bool PAIR>
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  if constexpr (PAIR) umma2_commit_mc(bar, 0x3);
-  else umma_commit(bar);
+__device__ __forceinline__ void commit(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)0x3)
+        : "memory");
+  else
+    commit_here<false>(bar);
 }
+
+// TMA loads to dst that complete on `bar` (of a pair, the leader's).
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], "
+        "[%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                        int c3) {
+  if constexpr (PAIR)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, "
+        "%6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+
+// Whether a phase is complete.
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// mbar_wait by address.
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, int* abort, int32_t* err, int site) {
+  return mbar_wait(static_cast<uint64_t*>(__cvta_shared_to_generic(bar)), parity, abort, err, site);
+}
+
+// A ring of stages as a thread steps through it: offset of the stage's barrier,
+// and the phase.
+struct Ring {
+  uint32_t bar, phase;
+  __device__ __forceinline__ Ring next(uint32_t bar_bytes) const {
+    const bool wrap = bar + 8 == bar_bytes;
+    return {wrap ? 0u : bar + 8u, phase ^ (wrap ? 1u : 0u)};
+  }
+};
 
 __device__ __forceinline__ void fence_to_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -217,20 +299,6 @@ __device__ __forceinline__ bool elect_one() {
 // mbar_wait of a whole warp, which stays converged.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* abort, int32_t* err, int site) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, err, site));
-}
-
-// Whether a phase is complete: issued before other work, it hides the 100 clocks
-// that even a wait for a phase long complete takes.
-__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}\n"
-      : "=r"(done)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
 }
 
 // Units per tile: the fewest rounds of tiles over the grid, each weighed by the
@@ -395,113 +463,100 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     // ---------------- TMA producer ----------------
     if (elect_one()) {
       const int stages = ring_stages(units, PAIR), sbytes = stage_bytes(units, PAIR);
-      int stage = 0, e = 0;
-      uint32_t phase = 0, issued = 0, last_parity = 0;
-      bool ok = true;
+      const uint32_t ring = smem_u32(base), full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
+      const uint32_t load_bar = PAIR ? mapa_shared(full, 0) : full;  // the leader's barriers count a pair's bytes
+      uint32_t dst = ring;
+      Ring at{0, 0};
+      int steps = 0, e = 0;
+      bool ok = true, seen = false;
       const CUtensorMap* tmB = &maps.b[PAIR ? 0 : units - 1];
-      bool seen = false;
       for (int tile = worker; ok && tile < total; tile += workers) {
         const Tile t = decode<PAIR>(ctl, args.E, units, n_tiles, tile, e, rank);
         e = t.e;
-        // boxes of A that the rows from row0 on fill, and their bytes
+        // boxes of A that the rows from row0 on fill
         auto boxes_from = [&](int row0) {
           return max(0, min(BM / A_BOX_ROWS, (t.row_end - row0 + A_BOX_ROWS - 1) / A_BOX_ROWS));
         };
+        constexpr uint32_t box_bytes = A_BYTES * A_BOX_ROWS / BM;
         const int boxes = boxes_from(t.row0);
         const bool whole = boxes == BM / A_BOX_ROWS;
-        // A pair's bytes are all counted by the leader's barrier.
-        const uint32_t bytes = (uint32_t)((boxes + (PAIR ? boxes_from(t.row0 + BM) : 0)) * (A_BYTES * A_BOX_ROWS / BM) +
-                                          units * UNIT_BYTES);
-        const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT);
-        for (int kt = 0; kt < args.k_steps; ++kt) {
-          if (!seen && !mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 1)) {
+        const uint32_t bytes = (boxes + (PAIR ? boxes_from(t.row0 + BM) : 0)) * box_bytes + units * UNIT_BYTES;
+        // W's rows of the tile; a pair loads half each, in gate_up the leader the gate rows and its peer the up rows
+        const int n0 = t.unit0 * (is_swiglu(MODE) ? UNIT / 2 : UNIT) +
+                       (PAIR && !is_swiglu(MODE) ? rank * (MAX_UNITS * UNIT / 2) : 0);
+        const int half = PAIR && is_swiglu(MODE) ? rank : 0;
+        for (int kb = 0; kb < args.k_steps * (BK / 2); kb += BK / 2) {
+          if (!seen && !bar_wait(empty + at.bar, at.phase ^ 1u, &ctl->abort, args.err, 1)) {
             ok = false;
             break;
           }
-          const int next = stage + 1 == stages ? 0 : stage + 1;
-          const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
-          seen = mbar_test(&ctl->empty[next], next_phase ^ 1u);
-          uint8_t* sa = base + stage * sbytes;
-          const int kb = kt * (BK / 2);
-          if constexpr (PAIR) {
-            const uint32_t full = mapa_shared(smem_u32(&ctl->full[stage]), 0);
-            if (leader) mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-            // gate_up: the leader loads the gate rows, its peer the up rows
-            tma2_load_4d(sa + A_BYTES, tmB, full, kb, is_swiglu(MODE) ? n0 : n0 + rank * (MAX_UNITS * UNIT / 2),
-                         is_swiglu(MODE) ? rank : 0, t.e);
-            if (whole) {
-              tma2_load_2d(sa, &maps.a_tile, full, kb, t.row0);
-            } else {
-              for (int i = 0; i < boxes; ++i)
-                tma2_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, full, kb, t.row0 + A_BOX_ROWS * i);
-            }
+          const Ring next = at.next(8 * stages);
+          seen = bar_test(empty + next.bar, next.phase ^ 1u);
+          if (!PAIR || leader) bar_expect(full + at.bar, bytes);
+          load_4d<PAIR>(dst + A_BYTES, tmB, load_bar + at.bar, kb, n0, half, e);
+          if (whole) {
+            load_2d<PAIR>(dst, &maps.a_tile, load_bar + at.bar, kb, t.row0);
           } else {
-            mbar_arrive_expect_tx(&ctl->full[stage], bytes);
-            tma_load_4d(sa + A_BYTES, tmB, &ctl->full[stage], kb, n0, 0, t.e);
-            if (whole) {
-              tma_load_2d(sa, &maps.a_tile, &ctl->full[stage], kb, t.row0);
-            } else {
-              for (int i = 0; i < boxes; ++i)
-                tma_load_2d(sa + i * (A_BYTES * A_BOX_ROWS / BM), &maps.a_box, &ctl->full[stage], kb,
-                            t.row0 + A_BOX_ROWS * i);
-            }
+            for (int i = 0; i < boxes; ++i)
+              load_2d<PAIR>(dst + i * box_bytes, &maps.a_box, load_bar + at.bar, kb, t.row0 + A_BOX_ROWS * i);
           }
-          issued |= 1u << stage;
-          last_parity = (last_parity & ~(1u << stage)) | (phase << stage);
-          stage = next;
-          phase = next_phase;
+          dst = next.bar == 0 ? ring : dst + sbytes;
+          at = next;
+          ++steps;
         }
       }
       // Every copy has landed before the CTA may exit (a pair's leader counts
       // both CTAs' bytes, and the CTAs exit together).
-      for (int s = 0; s < stages; ++s)
-        if (leader && ((issued >> s) & 1u))
-          mbar_wait(&ctl->full[s], (last_parity >> s) & 1u, &ctl->abort, args.err, 6, true);
+      if (!PAIR || leader)
+        for (int s = max(0, steps - stages); s < steps; ++s)
+          mbar_wait(&ctl->full[s % stages], (uint32_t)(s / stages) & 1u, &ctl->abort, args.err, 6, true);
     }
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
     if (leader && elect_one()) {
-      const int stages = ring_stages(units, PAIR), sbytes = stage_bytes(units, PAIR);
-      const uint32_t smem_base = smem_u32(base);
+      const int stages = ring_stages(units, PAIR);
+      const uint32_t desc_step = stage_bytes(units, PAIR) / 16, sf_step = sf_cols(units), sfb_step = 4 * blocks;
+      const uint32_t full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
+      const uint32_t desc0 = desc_low(smem_u32(base)), sf0 = tmem_base + SF_COL;
       constexpr int M = PAIR ? 2 * BM : BM;
       const uint32_t idesc0 = make_idesc_mxf4(M, units * UNIT, 0), idesc2 = make_idesc_mxf4(M, units * UNIT, 2);
       const int k_tail = args.K - (args.k_steps - 1) * BK;  // values of the last step
-      int stage = 0, acc = 0;
-      uint32_t phase = 0, acc_phase = 0;
+      uint32_t adesc = desc0, sfa = sf0, acc_phase = 0;
+      Ring at{0, 0};
+      int acc = 0;
       bool ok = true, seen = false;
       for (int tile = worker; ok && tile < total; tile += workers) {
         if (!mbar_wait(&ctl->tempty[acc], acc_phase ^ 1u, &ctl->abort, args.err, 2)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + (uint32_t)(acc * ACC_COLS);
-        for (int kt = 0; kt < args.k_steps; ++kt) {
-          if (!seen && !mbar_wait(&ctl->full[stage], phase, &ctl->abort, args.err, 3)) {
+        uint32_t accumulate = 0;
+        for (int kt = args.k_steps; kt > 0; --kt) {
+          if (!seen && !bar_wait(full + at.bar, at.phase, &ctl->abort, args.err, 3)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const int next = stage + 1 == stages ? 0 : stage + 1;
-          const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
-          seen = mbar_test(&ctl->full[next], next_phase);
-          const uint32_t sa = smem_base + stage * sbytes;
-          const uint32_t sfa = tmem_base + SF_COL + stage * sf_cols(units), sfb = sfa + SFB_COL;
-          const uint64_t adesc = sw128_desc(sa), bdesc = sw128_desc(sa + A_BYTES);
-          const bool last = kt + 1 == args.k_steps;
-          const int left = last ? k_tail : BK;
-          umma_mxf4<PAIR>(d_tmem, adesc, bdesc, idesc0, sfa, sfb, kt > 0 ? 1u : 0u);
+          const Ring next = at.next(8 * stages);
+          seen = bar_test(full + next.bar, next.phase);
+          const uint32_t bdesc = adesc + A_BYTES / 16, sfb = sfa + SFB_COL;
+          const int left = kt == 1 ? k_tail : BK;
+          umma_mxf4<PAIR>(d_tmem, adesc, bdesc, idesc0, sfa, sfb, accumulate);
           if (left > 64) umma_mxf4<PAIR>(d_tmem, adesc + 2, bdesc + 2, idesc2, sfa, sfb, 1u);
-          if (left > 128) umma_mxf4<PAIR>(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + 4 * blocks, 1u);
-          if (left > 192) umma_mxf4<PAIR>(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + 4 * blocks, 1u);
-          commit<PAIR>(&ctl->empty[stage]);
-          stage = next;
-          phase = next_phase;
+          if (left > 128) umma_mxf4<PAIR>(d_tmem, adesc + 4, bdesc + 4, idesc0, sfa + 4, sfb + sfb_step, 1u);
+          if (left > 192) umma_mxf4<PAIR>(d_tmem, adesc + 6, bdesc + 6, idesc2, sfa + 4, sfb + sfb_step, 1u);
+          commit<PAIR>(empty + at.bar);
+          accumulate = 1;
+          adesc = next.bar == 0 ? desc0 : adesc + desc_step;
+          sfa = next.bar == 0 ? sf0 : sfa + sf_step;
+          at = next;
         }
         if (!ok) break;
-        commit<PAIR>(&ctl->tfull[acc]);
+        commit<PAIR>(smem_u32(&ctl->tfull[acc]));
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
       }
-      commit<PAIR>(&ctl->drain);
+      commit<PAIR>(smem_u32(&ctl->drain));
       mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     }
     if (PAIR && !leader) mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
@@ -512,43 +567,43 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     // MMA issuer's time. Every stage of the operands has its columns, so that a
     // step's copies complete its full barrier like its operands.
     if (leader && elect_one()) {
-      const int stages = ring_stages(units, PAIR), sf_bytes = sf_stage_bytes(units);
-      const uint32_t sf_smem = smem_u32(sf_base);
-      int stage = 0, sf_stage = 0;
-      uint32_t phase = 0, sf_phase = 0;
+      const int stages = ring_stages(units, PAIR);
+      const uint32_t desc_step = sf_stage_bytes(units) / 16, sf_step = sf_cols(units);
+      const uint32_t full = smem_u32(ctl->full), empty = smem_u32(ctl->empty);
+      const uint32_t sfull = smem_u32(ctl->sfull), sempty = smem_u32(ctl->sempty);
+      const uint32_t desc0 = desc_low(smem_u32(sf_base)), sf0 = tmem_base + SF_COL;
+      constexpr uint32_t kAtom = SF_ATOM_BYTES / 16;
+      uint32_t desc = desc0, sfa = sf0;
+      Ring at{0, 0}, sf{0, 0};
       bool ok = true;
       for (int tile = worker; ok && tile < total; tile += workers) {
         for (int kt = 0; kt < args.k_steps; ++kt) {
-          ok = mbar_wait(&ctl->empty[stage], phase ^ 1u, &ctl->abort, args.err, 9) &&
-               ((kt & 1) || mbar_wait(&ctl->sfull[sf_stage], sf_phase, &ctl->abort, args.err, 10));
+          ok = bar_wait(empty + at.bar, at.phase ^ 1u, &ctl->abort, args.err, 9) &&
+               ((kt & 1) || bar_wait(sfull + sf.bar, sf.phase, &ctl->abort, args.err, 10));
           if (!ok) break;
           tc_fence_after();
-          const uint32_t sfa = tmem_base + SF_COL + stage * sf_cols(units), sfb = sfa + SFB_COL;
-          const uint64_t da = sf_desc(sf_smem + sf_stage * sf_bytes + (kt & 1) * 2 * SF_ATOM_BYTES);
-          const uint64_t db = sf_desc(sf_smem + sf_stage * sf_bytes + (4 + (kt & 1) * 2 * blocks) * SF_ATOM_BYTES);
+          // the step's two atoms of A, and of B after A's four
+          const uint32_t sfb = sfa + SFB_COL, da = desc + (kt & 1) * 2 * kAtom;
+          const uint32_t db = desc + (4 + (kt & 1) * 2 * blocks) * kAtom;
           copy_scales<PAIR>(sfa, da);
-          copy_scales<PAIR>(sfa + 4, da + SF_ATOM_BYTES / 16);
+          copy_scales<PAIR>(sfa + 4, da + kAtom);
           copy_scales<PAIR>(sfb, db);
-          copy_scales<PAIR>(sfb + 4, db + SF_ATOM_BYTES / 16);
+          copy_scales<PAIR>(sfb + 4, db + kAtom);
           if (blocks == 2) {
-            copy_scales<PAIR>(sfb + 8, db + 2 * (SF_ATOM_BYTES / 16));
-            copy_scales<PAIR>(sfb + 12, db + 3 * (SF_ATOM_BYTES / 16));
+            copy_scales<PAIR>(sfb + 8, db + 2 * kAtom);
+            copy_scales<PAIR>(sfb + 12, db + 3 * kAtom);
           }
-          commit_here<PAIR>(&ctl->full[stage]);
-          if (++stage == stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          commit_here<PAIR>(full + at.bar);
+          at = at.next(8 * stages);
+          sfa = at.bar == 0 ? sf0 : sfa + sf_step;
           if ((kt & 1) || kt + 1 == args.k_steps) {
-            commit<PAIR>(&ctl->sempty[sf_stage]);
-            if (++sf_stage == SF_STAGES) {
-              sf_stage = 0;
-              sf_phase ^= 1u;
-            }
+            commit<PAIR>(sempty + sf.bar);
+            sf = sf.next(8 * SF_STAGES);
+            desc = sf.bar == 0 ? desc0 : desc + desc_step;
           }
         }
       }
-      commit<PAIR>(&ctl->cdrain);
+      commit<PAIR>(smem_u32(&ctl->cdrain));
       mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
     }
     if (PAIR && !leader) mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
