@@ -160,6 +160,13 @@ class Problem:
                            SCORES[self.score], BIAS_MODES[self.bias_mode], int(bool(self.renormalize)),
                            SHARED_KINDS[self.shared], 0)
 
+    def _struct(self) -> moe_problem:
+        """c(), made once for calls that only read it."""
+        s = self.__dict__.get("_c")
+        if s is None:
+            s = self.__dict__["_c"] = self.c()
+        return s
+
     @property
     def torch_dtype(self) -> torch.dtype:
         return TORCH_DTYPE[self.dtype]

@@ -122,7 +122,7 @@ def mx4_permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]) -> Mx4:
     dev = x.device
     pair_pos, offsets = _plan(p, plan, dev.index)
     q = _new((p.T * p.k,), p.H, dev)
-    _launch(lib().moe_mx4_permute_rows, dev, p.c(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(),
+    _launch(lib().moe_mx4_permute_rows, dev, p._struct(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(),
             q.data.data_ptr(), q.scale.data_ptr())
     return q
 
@@ -236,12 +236,12 @@ class Mx4SparseMoE(SparseMoE):
         _req_at(sel, "selected_experts", (p.T, p.k), torch.int64, dev.index)
         gate = w.get("shared_gate")
         gamma = None if gate is None else torch.empty(p.T, dtype=torch.float32, device=dev)
-        _launch(lib().moe_route, dev, p.c(), x.data_ptr(), w["gate_w"].data_ptr(), _ptr(w.get("bias")), _ptr(gate),
+        _launch(lib().moe_route, dev, p._struct(), x.data_ptr(), w["gate_w"].data_ptr(), _ptr(w.get("bias")), _ptr(gate),
                 rw.data_ptr(), sel.data_ptr(), _ptr(gamma), ws.data_ptr(), ws.numel())
         # the counts stay in one buffer, so that a replayed graph's are the last forward's too
         table = torch.empty(p.E + 1, dtype=torch.int32, device=dev)
         pairs, pos = (torch.empty(p.T * p.k, dtype=torch.int32, device=dev) for _ in range(2))
-        _launch(lib().moe_dispatch, dev, p.c(), sel.data_ptr(), None, self._counts.data_ptr(), table.data_ptr(),
+        _launch(lib().moe_dispatch, dev, p._struct(), sel.data_ptr(), None, self._counts.data_ptr(), table.data_ptr(),
                 pairs.data_ptr(), pos.data_ptr(), None, ws.data_ptr(), ws.numel())
         rows = mx4_permute_rows(p, x, {"pair_pos": pos, "offsets": table})
         h = mx4_grouped_gate_up(rows, w["gate_up"], table, quantize=True, ws=ws)
@@ -249,9 +249,9 @@ class Mx4SparseMoE(SparseMoE):
         shared = None
         if p.shared != "none":
             shared = torch.empty(p.T, p.H, dtype=torch.float32, device=dev)
-            _launch(lib().moe_shared_expert, dev, p.c(), x.data_ptr(), w["shared_gate_up"].data_ptr(),
+            _launch(lib().moe_shared_expert, dev, p._struct(), x.data_ptr(), w["shared_gate_up"].data_ptr(),
                     w["shared_down"].data_ptr(), _ptr(gamma), shared.data_ptr(), ws.data_ptr(), ws.numel())
-        _launch(lib().moe_unpermute_rows, dev, p.c(), DTYPES["bf16"], y.data_ptr(), pos.data_ptr(), rw.data_ptr(),
+        _launch(lib().moe_unpermute_rows, dev, p._struct(), DTYPES["bf16"], y.data_ptr(), pos.data_ptr(), rw.data_ptr(),
                 _ptr(shared), out.data_ptr())
         return out, rw, sel
 

@@ -57,21 +57,21 @@ def _req_y(p: Problem, y_perm) -> int:
 def _permute(p: Problem, x, pair_pos, offsets):
     dev = x.device
     out = torch.empty(p.T * p.k, p.H, dtype=x.dtype, device=dev)
-    _launch(lib().moe_permute_rows, dev, p.c(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    _launch(lib().moe_permute_rows, dev, p._struct(), x.data_ptr(), pair_pos.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
 def _permute_backward(p: Problem, dx_perm, pair_pos):
     dev = dx_perm.device
     dx = torch.empty(p.T, p.H, dtype=dx_perm.dtype, device=dev)
-    _launch(lib().moe_permute_rows_backward, dev, p.c(), dx_perm.data_ptr(), pair_pos.data_ptr(), dx.data_ptr())
+    _launch(lib().moe_permute_rows_backward, dev, p._struct(), dx_perm.data_ptr(), pair_pos.data_ptr(), dx.data_ptr())
     return dx
 
 
 def _unpermute(p: Problem, yd: int, y_perm, pair_pos, routing_weights, shared_out):
     dev = y_perm.device
     out = torch.empty(p.T, p.H, dtype=TORCH_DTYPE[p.dtype], device=dev)
-    _launch(lib().moe_unpermute_rows, dev, p.c(), yd, y_perm.data_ptr(), pair_pos.data_ptr(), _ptr(routing_weights),
+    _launch(lib().moe_unpermute_rows, dev, p._struct(), yd, y_perm.data_ptr(), pair_pos.data_ptr(), _ptr(routing_weights),
             _ptr(shared_out), out.data_ptr())
     return out
 
@@ -83,7 +83,7 @@ def _unpermute_backward(p: Problem, yd: int, dout, y_perm, pair_pos, offsets, ro
                      device=dev) if rows else None
     dw = torch.empty(p.T, p.k, dtype=torch.float32, device=dev) if weights else None
     if rows or weights:
-        _launch(lib().moe_unpermute_rows_backward, dev, p.c(), yd, dout.data_ptr(), _ptr(y_perm), pair_pos.data_ptr(),
+        _launch(lib().moe_unpermute_rows_backward, dev, p._struct(), yd, dout.data_ptr(), _ptr(y_perm), pair_pos.data_ptr(),
                 offsets.data_ptr(), _ptr(routing_weights), _ptr(dy), _ptr(dw))
     return dy, dw
 

@@ -10,6 +10,7 @@ so K/32 + 2 such steps bound it. Rounding to bf16 adds 2^-8 of the value. SwiGLU
 |d silu/dg| <= 1.1, and exp, the division and the products in fp32 lose at most
 2^-20 of the result."""
 
+import dataclasses
 import random
 
 import pytest
@@ -420,6 +421,41 @@ def test_a_malformed_table_is_reported_and_computes_nothing():
         assert stm.read_device_error(ws) == stm.DEVERR_BAD_EXPERT_ID
 
 
+def test_sizes_beyond_32_bits():
+    """Elements and bytes past 2^31 and 2^32, checked at both ends."""
+    K = 64
+    rows = (1 << 31) // K + 1000
+    x = torch.randn(1000, K, device="cuda").bfloat16().repeat(rows // 1000 + 1, 1)[:rows].contiguous()
+    q = stm.mx4_quantize(x)
+    want = stm.mx4_quantize(x[:1000].contiguous())
+    for at in (0, rows // 1000 * 1000 - 1000):
+        assert torch.equal(q.data[at:at + 1000], want.data) and torch.equal(q.scale[at:at + 1000], want.scale)
+    del x
+    back = q.dequantize()
+    assert torch.equal(back[-1000 - rows % 1000:][:1000], want.dequantize())
+    del q, back
+    # a product of more outputs than 2^31
+    rows, N = 270000, 8192
+    a, w = _operands(1000, 2, N, 32, 1)
+    a = stm.Mx4(a.data.repeat(270, 1), a.scale.repeat(270, 1))
+    off = torch.tensor([0, 1000, rows], dtype=torch.int32, device="cuda")
+    y = stm.mx4_grouped_matmul(a, w, off)
+    small = stm.mx4_grouped_matmul(stm.Mx4(a.data[:1000], a.scale[:1000]), stm.Mx4(w.data[1:], w.scale[1:]),
+                                   torch.tensor([0, 1000], dtype=torch.int32, device="cuda"))
+    assert torch.equal(y[-1000:], small) and torch.equal(y[1000:2000], small)
+    del y
+    # weights of more than 2^32 bytes
+    E, N, K = 256, 16384, 2112
+    a, w = _operands(100, 1, N, K, 2)
+    big = stm.Mx4(torch.zeros(E, N, K // 2, dtype=torch.uint8, device="cuda"),
+                  torch.zeros(E, N, w.scale.shape[-1], dtype=torch.uint8, device="cuda"))
+    big.data[E - 1], big.scale[E - 1] = w.data[0], w.scale[0]
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[E] = 100
+    got = stm.mx4_grouped_matmul(a, big, off, torch.float32)
+    assert torch.equal(got, stm.mx4_grouped_matmul(a, w, off[-2:].clone(), torch.float32))
+
+
 def test_no_rows_and_no_used_experts():
     a, w = _operands(10, 3, 64, 64, 1)
     off = torch.zeros(4, dtype=torch.int32, device="cuda")
@@ -516,7 +552,7 @@ def test_layer_counts_after_a_replay_are_the_replays():
 
 def test_layer_without_tokens():
     p, dev, _ = _layer("dsv4")
-    p0 = stm.Problem(**{**p.__dict__, "T": 0})
+    p0 = dataclasses.replace(p, T=0)
     moe = stm.Mx4SparseMoE(p0, dev)
     out, rw, sel = moe(dev["x"][:0].contiguous())
     assert out.shape == (0, p.H) and rw.shape == (0, p.k) and sel.shape == (0, p.k)

@@ -132,6 +132,22 @@ def test_every_number_of_slots(shape, dtype, y_dtype):
     test_permute_and_its_gradient(shape, dtype, 0.3)
 
 
+def test_rows_beyond_32_bits():
+    """More than 2^31 sorted elements: row movement there and back, checked whole."""
+    p = _problem((40000, 7168, 16, 8))
+    _, plan = _plan(p, 0.0)
+    x = torch.randn(p.T, p.H, device="cuda").bfloat16()
+    rows = stm.permute_rows(p, x, plan)
+    w = torch.full((p.T, p.k), 0.125, device="cuda")
+    assert torch.equal(stm.unpermute_rows(p, rows, plan, w), x)  # eight equal rows times 1/8: exact
+    at = plan["pair_pos"].long()
+    assert torch.equal(rows[at[-8:]], x[-1:].expand(8, -1))
+    dy, dw = stm.unpermute_rows_backward(p, x, rows, plan, w)
+    assert torch.equal(dy[at[-8:]], (x[-1:] * 0.125).expand(8, -1))
+    norm = (x.double() ** 2).sum(1)
+    assert bool(((dw.double() - norm[:, None]).abs() <= p.H * 2.0 ** -23 * norm[:, None]).all())
+
+
 def test_infinite_and_nan_rows_stay_in_their_token():
     p = _problem((40, 64, 8, 2))
     sel, plan = _plan(p, 0.0)
