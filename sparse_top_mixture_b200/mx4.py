@@ -81,8 +81,9 @@ def _req_mx4(q: Mx4, name: str, lead: Optional[Sequence[int]] = None) -> int:
 
 
 def _new(lead: Tuple[int, ...], K: int, device) -> Mx4:
-    return Mx4(torch.empty(lead + (K // 2,), dtype=torch.uint8, device=device),
-               torch.empty(lead + (_scale_bytes(K),), dtype=torch.uint8, device=device))
+    # (sizes as arguments of their own: a tuple of them costs torch another 0.7 us)
+    return Mx4(torch.empty(*lead, K // 2, dtype=torch.uint8, device=device),
+               torch.empty(*lead, _scale_bytes(K), dtype=torch.uint8, device=device))
 
 
 def mx4_quantize(x: torch.Tensor) -> Mx4:
@@ -108,7 +109,7 @@ def mx4_dequantize(q: Mx4, dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
     if dtype not in _DTYPE_ID:
         raise ValueError(f"dtype {dtype}, expected bf16 or fp32")
     dev = q.data.device
-    out = torch.empty(q.data.shape[:-1] + (K,), dtype=dtype, device=dev)
+    out = torch.empty(*q.data.shape[:-1], K, dtype=dtype, device=dev)
     _launch(lib().moe_mx4_dequantize, dev, out.numel() // K, K, _DTYPE_ID[dtype], q.data.data_ptr(),
             q.scale.data_ptr(), out.data_ptr())
     return out
