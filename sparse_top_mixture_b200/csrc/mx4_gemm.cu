@@ -913,10 +913,11 @@ cudaError_t launch_product(int64_t rows, int64_t E, int64_t N, int64_t K, const 
 
 bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// rows, E, N, K of a product; tiles are counted in 32 bits.
+// rows, E, N, K of a product; rows and tiles are counted in 32 bits, and the last
+// tile of a segment that ends at the last row reaches up to 2 * BM - 1 rows past it.
 moe_status check_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, int64_t n_multiple) {
   const int64_t lim = int64_t(1) << 31;
-  if (rows < 0 || rows >= lim || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= lim)
+  if (rows < 0 || rows >= lim - 2 * BM || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= lim)
     return MOE_ERR_INVALID_ARGUMENT;
   if (K % mx4::kBlock != 0 || N % n_multiple != 0) return MOE_ERR_INVALID_ARGUMENT;
   if ((rows / BM + E) * ceil_div(N, 32) >= lim - 4096) return MOE_ERR_INVALID_ARGUMENT;  // a round of tiles beyond

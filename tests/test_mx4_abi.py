@@ -62,3 +62,49 @@ def test_grouped_gate_up_validates():
             assert call(4, 4, 64, 64, *[bad if j == i else A for j in range(6)], A, None, None) == 1
     assert call(4, 4, 64, 64, *[A] * 6, 8, None, None) == 1
     assert call(0, 4, 64, 64, *[None] * 6, None, None, None) == 0
+
+
+def _tile_table(offsets, BM):
+    """csrc/tiles.cuh and the rows that mx4_gemm.cu makes of it, in wrapped 32 bits: (row tiles of each segment, the
+    largest row that a lane of any segment's last tile compares with the segment's end)."""
+    import numpy as np
+
+    with np.errstate(over="ignore"):
+        a, b, m = (np.array(v, dtype=np.int32) for v in (offsets[:-1], offsets[1:], BM))
+        counts = (b - a + m - np.int32(1)) // m
+        last = a + (counts - np.int32(1)) * m + m - np.int32(1)
+    return counts.tolist(), last.tolist()
+
+
+def _statuses_without_a_device(sizes):
+    """Of both products for each (rows, K), in a process that sees no GPU: 1 where the sizes are refused, another error
+    (no device) where they are accepted. Nothing can be launched there."""
+    import os
+    import subprocess
+    import sys
+
+    code = (f"import sparse_top_mixture_b200 as stm; L = stm.lib(); A = 16\n"
+            f"for rows, K in {sizes}:\n"
+            f"    print(L.moe_mx4_grouped_matmul(rows, 1, 8, K, 1, *[A] * 6, None, None),"
+            f" L.moe_mx4_grouped_gate_up(rows, 1, 32, K, *[A] * 6, None, None, None))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], env={**os.environ, "CUDA_VISIBLE_DEVICES": ""}, cwd=root,
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
+    return [[int(v) for v in line.split()] for line in r.stdout.splitlines()]
+
+
+def test_rows_next_to_32_bits():
+    """Where rows or tiles would wrap, the products refuse; the largest accepted count wraps nowhere."""
+    shorts = [0, 1, 127, 128, 255, 256]
+    statuses = _statuses_without_a_device([((1 << 31) - 1 - short, 32) for short in shorts])
+    for short, status in zip(shorts, statuses):
+        rows = (1 << 31) - 1 - short
+        wraps = False
+        for offsets in ([0, rows], [0, 1, rows], [0, rows - 1, rows]):
+            for BM in (128, 256):
+                counts, last = _tile_table(offsets, BM)
+                wraps |= any(c != -(-(b - a) // BM) for a, b, c in zip(offsets, offsets[1:], counts))
+                wraps |= any(b > a and row < b - 1 for a, b, row in zip(offsets, offsets[1:], last))
+        assert wraps == (short < 255)
+        assert (status == [1, 1]) == (short < 256)
