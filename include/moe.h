@@ -527,8 +527,8 @@ moe_status moe_unpermute_rows_backward(const moe_problem *p, int32_t y_dtype, co
  * nearest code, ties to the even one, beyond 6 to 6; a block with an infinity
  * or a NaN gets b = 255 and code 0. The power-of-two products are exact, so a
  * given block has one result.
- * Sizes are below 2^31 (a product's rows below 2^31 - 256, and its tiles,
- * (rows/128 + E) * N/32, below 2^31 - 4096);
+ * Sizes are below 2^31 (a product's rows below 2^31 - 256, its K (H) below
+ * 2^27, and its tiles, (rows/128 + E) * N/32, below 2^31 - 4096);
  * async on `stream`; the calls can be captured.
  *   moe_mx4_quantize: x [rows, K] (dtype: a moe_dtype) to data and scale.
  *   moe_mx4_dequantize: data and scale to out [rows, K] (dtype), code times

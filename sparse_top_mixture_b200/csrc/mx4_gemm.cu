@@ -915,9 +915,13 @@ bool ok_ptr(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>
 
 // rows, E, N, K of a product; rows and tiles are counted in 32 bits, and the last
 // tile of a segment that ends at the last row reaches up to 2 * BM - 1 rows past it.
+// K: the second accumulator's epilogue waits for two whole tiles, and a wait gives
+// up after 2e9 clocks; a step of 256 that streams its operands from HBM takes some
+// 1300, so the 2^20 steps of two tiles of 2^27 stay below it.
+constexpr int64_t kMaxK = int64_t(1) << 27;
 moe_status check_sizes(int64_t rows, int64_t E, int64_t N, int64_t K, int64_t n_multiple) {
   const int64_t lim = int64_t(1) << 31;
-  if (rows < 0 || rows >= lim - 2 * BM || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= lim)
+  if (rows < 0 || rows >= lim - 2 * BM || E < 1 || E > kMaxExperts || N < 1 || N >= lim / 4 || K < 1 || K >= kMaxK)
     return MOE_ERR_INVALID_ARGUMENT;
   if (K % mx4::kBlock != 0 || N % n_multiple != 0) return MOE_ERR_INVALID_ARGUMENT;
   if ((rows / BM + E) * ceil_div(N, 32) >= lim - 4096) return MOE_ERR_INVALID_ARGUMENT;  // a round of tiles beyond

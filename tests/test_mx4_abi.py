@@ -108,3 +108,9 @@ def test_rows_next_to_32_bits():
                 wraps |= any(b > a and row < b - 1 for a, b, row in zip(offsets, offsets[1:], last))
         assert wraps == (short < 255)
         assert (status == [1, 1]) == (short < 256)
+
+
+def test_rows_too_long_for_the_bounded_waits():
+    """A K of 2^27 or more, whose tiles could outlast a wait, is refused."""
+    assert _statuses_without_a_device([(4, 1 << 27)]) == [[1, 1]]
+    assert all(s not in (0, 1) for s in _statuses_without_a_device([(4, (1 << 27) - 32)])[0])
