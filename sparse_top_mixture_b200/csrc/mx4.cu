@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(QTHREADS) quantize_kernel(const T* __restrict_
         *reinterpret_cast<uint4*>(data + r * (K / 8) + col / 8) = code;
         s[col / kBlock] = (uint8_t)b;
       }
-      if (c0 + kChunk >= K && pad0 + lane < pitch) s[pad0 + lane] = 0;
+      if (K - c0 <= kChunk && pad0 + lane < pitch) s[pad0 + lane] = 0;
     };
     if constexpr (SORTED) {
 #pragma unroll

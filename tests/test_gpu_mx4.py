@@ -114,6 +114,19 @@ def test_dequantize_every_code_and_scale():
         assert same(q.dequantize(out).double().cpu(), v.to(out).double())
 
 
+def test_the_padding_of_the_longest_rows_is_written():
+    """K next to 2^31, where a row's last chunk ends past 32 bits."""
+    K = (1 << 31) - 32
+    x = torch.ones(1, K, dtype=torch.bfloat16, device="cuda")
+    data = torch.empty(1, K // 2, dtype=torch.uint8, device="cuda")
+    scale = torch.full((1, 1 << 26), 9, dtype=torch.uint8, device="cuda")
+    st = stm.lib().moe_mx4_quantize(1, K, stm.DTYPES["bf16"], x.data_ptr(), data.data_ptr(), scale.data_ptr(),
+                                    torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    assert bool((scale[0, :-1] == 125).all()) and int(scale[0, -1]) == 0  # 2^-2, and one byte of padding
+    assert bool((data == 0x66).all())  # 4 = 1 / 2^-2
+
+
 def test_quantize_shapes():
     x = _rand((3, 5, 64))
     q = stm.mx4_quantize(x)
