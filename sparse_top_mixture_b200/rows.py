@@ -88,6 +88,12 @@ def _unpermute_backward(p: Problem, yd: int, dout, y_perm, pair_pos, offsets, ro
     return dy, dw
 
 
+def _whole(t: torch.Tensor) -> torch.Tensor:
+    """t contiguous and on a 16-byte boundary: autograd may hand on a view of any strides and offset."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class _PermuteRows(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, p, pair_pos, offsets):
@@ -99,7 +105,7 @@ class _PermuteRows(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dx_perm):
         (pair_pos,) = ctx.saved_tensors
-        return _permute_backward(ctx.p, dx_perm.contiguous(), pair_pos), None, None, None
+        return _permute_backward(ctx.p, _whole(dx_perm), pair_pos), None, None, None
 
 
 class _UnpermuteRows(torch.autograd.Function):
@@ -114,7 +120,7 @@ class _UnpermuteRows(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dout):
         y_perm, routing_weights, pair_pos, offsets = ctx.saved_tensors
-        dout = dout.contiguous()
+        dout = _whole(dout)
         rows, weights, shared = ctx.needs_input_grad[:3]
         dy, dw = _unpermute_backward(ctx.p, ctx.yd, dout, y_perm, pair_pos, offsets, routing_weights, rows, weights)
         return dy, dw, dout.float() if shared else None, None, None, None, None

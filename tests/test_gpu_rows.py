@@ -335,6 +335,30 @@ def test_gradients_of_outputs_that_are_views():
         assert torch.equal(x.grad, stm.permute_rows_backward(p, dy, plan))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("front", [1, 3, 8])
+def test_gradients_at_any_offset(front, dtype):
+    """A gradient that autograd cuts out of a longer one: contiguous, at an offset of `front` elements."""
+    p = _problem((16, 40, 4, 2), dtype)
+    _, plan = _plan(p, 0.2)
+    w = torch.rand(p.T, p.k, device="cuda", requires_grad=True)
+    x = _rand((p.T, p.H), p.torch_dtype, 1).cuda().requires_grad_(True)
+    a = torch.zeros(front, dtype=p.torch_dtype, device="cuda", requires_grad=True)
+
+    def cut(t, seed):
+        g = _rand((front + t.numel(),), p.torch_dtype, seed).cuda()
+        torch.cat([a, t.reshape(-1)]).backward(g)
+        return g[front:].view(t.shape).clone()
+
+    rows = stm.permute_rows(p, x, plan)
+    dxp = cut(rows, 2)
+    assert torch.equal(x.grad, stm.permute_rows_backward(p, dxp, plan))
+    y = rows.detach().requires_grad_(True)
+    dout = cut(stm.unpermute_rows(p, y, plan, w), 3)
+    dy, dw = stm.unpermute_rows_backward(p, dout, y.detach(), plan, w.detach())
+    assert torch.equal(y.grad, dy) and torch.equal(w.grad, dw)
+
+
 def test_refusals():
     p = _problem((4, 32, 4, 2))
     _, plan = _plan(p, 0.0)
