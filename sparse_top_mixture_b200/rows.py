@@ -4,7 +4,8 @@ For experts of the caller's own between the library's dispatch and its
 weighted return: ``permute_rows`` copies each token's row to its k segment
 slots, ``unpermute_rows`` sums a token's k rows with the routing weights. Both
 take part in autograd (in ``x``; in ``y_perm``, ``routing_weights`` and
-``shared_out``); ``permute_rows_backward`` and ``unpermute_rows_backward`` are
+``shared_out``), once and in reverse mode: tensors with a forward-mode tangent
+are refused. ``permute_rows_backward`` and ``unpermute_rows_backward`` are
 their gradients as plain calls. The plan is what ``dispatch`` or
 ``dispatch_slots`` returned for the same problem.
 
@@ -25,6 +26,7 @@ from __future__ import annotations
 from typing import Dict, Optional, Tuple
 
 import torch
+from torch.autograd import forward_ad
 
 from . import DTYPES, TORCH_DTYPE, Problem, _launch, _ptr, _req, lib
 
@@ -94,7 +96,20 @@ def _whole(t: torch.Tensor) -> torch.Tensor:
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _tangent(*tensors: Optional[torch.Tensor]) -> bool:
+    """Whether one of them has a forward-mode tangent. (Such a tensor need not require a gradient, and a call past
+    autograd would drop the tangent; asked only while a level is open, which costs a call nothing.)"""
+    return getattr(forward_ad, "_current_level", 0) >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+def _no_jvp(*_):
+    raise NotImplementedError("permute_rows and unpermute_rows have no forward-mode derivative")
+
+
 class _PermuteRows(torch.autograd.Function):
+    jvp = staticmethod(_no_jvp)
+
     @staticmethod
     def forward(ctx, x, p, pair_pos, offsets):
         ctx.p = p
@@ -109,6 +124,8 @@ class _PermuteRows(torch.autograd.Function):
 
 
 class _UnpermuteRows(torch.autograd.Function):
+    jvp = staticmethod(_no_jvp)
+
     @staticmethod
     def forward(ctx, y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets):
         ctx.p, ctx.yd = p, yd
@@ -131,7 +148,7 @@ def permute_rows(p: Problem, x, plan: Dict[str, torch.Tensor]):
     positions. Rows past the last segment are zeros. Differentiable in x."""
     _req(x, "x", (p.T, p.H), TORCH_DTYPE[p.dtype])
     pair_pos, offsets = _plan(p, plan, x.get_device())
-    if x.requires_grad and torch.is_grad_enabled():
+    if (x.requires_grad and torch.is_grad_enabled()) or _tangent(x):
         return _PermuteRows.apply(x, p, pair_pos, offsets)
     return _permute(p, x, pair_pos, offsets)
 
@@ -160,7 +177,7 @@ def unpermute_rows(p: Problem, y_perm, plan: Dict[str, torch.Tensor], routing_we
     if shared_out is not None:
         _req_at(shared_out, "shared_out", (p.T, p.H), torch.float32, index)
         grad = grad or shared_out.requires_grad
-    if grad and torch.is_grad_enabled():
+    if (grad and torch.is_grad_enabled()) or _tangent(y_perm, routing_weights, shared_out):
         return _UnpermuteRows.apply(y_perm, routing_weights, shared_out, p, yd, pair_pos, offsets)
     return _unpermute(p, yd, y_perm, pair_pos, routing_weights, shared_out)
 

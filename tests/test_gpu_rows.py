@@ -359,6 +359,30 @@ def test_gradients_at_any_offset(front, dtype):
     assert torch.equal(y.grad, dy) and torch.equal(w.grad, dw)
 
 
+def test_forward_mode_is_refused():
+    """A tensor with a tangent need not require a gradient; its tangent must not be lost in silence."""
+    from torch.autograd import forward_ad
+
+    p = _problem((6, 32, 4, 2))
+    _, plan = _plan(p, 0.0)
+    x = _rand((p.T, p.H), torch.bfloat16, 1).cuda()
+    y = _rand((p.T * p.k, p.H), torch.bfloat16, 2).cuda()
+    w, shared = torch.rand(p.T, p.k, device="cuda"), torch.rand(p.T, p.H, device="cuda")
+    calls = [(lambda t: stm.permute_rows(p, t, plan), x), (lambda t: stm.unpermute_rows(p, t, plan, w), y),
+             (lambda t: stm.unpermute_rows(p, y, plan, t), w), (lambda t: stm.unpermute_rows(p, y, plan, w, t), shared)]
+    for call, t in calls:
+        with forward_ad.dual_level():
+            call(t)  # no tangent: nothing to refuse
+            for leaf in (t, t.clone().requires_grad_(True)):
+                dual = forward_ad.make_dual(leaf, torch.ones_like(t))
+                with pytest.raises(NotImplementedError, match="forward-mode"):
+                    call(dual)
+                with torch.no_grad(), pytest.raises(NotImplementedError, match="forward-mode"):
+                    call(dual)
+        with pytest.raises((NotImplementedError, RuntimeError)):
+            torch.func.jvp(call, (t,), (torch.ones_like(t),))
+
+
 def test_refusals():
     p = _problem((4, 32, 4, 2))
     _, plan = _plan(p, 0.0)
