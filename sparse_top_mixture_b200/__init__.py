@@ -177,6 +177,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 
 def _stream(device: Optional[torch.device] = None) -> int:
+    if device is not None and device.type != "cuda":
+        raise ValueError(f"expected a CUDA device, not {device}")
     index = None if device is None else device.index
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 

@@ -85,3 +85,14 @@ def test_a_launch_has_its_device_current_and_its_stream(monkeypatch, current):
     assert seen == [(5, None, 101, 1)] and state["device"] == current
     with pytest.raises(stm.MoeError):
         stm._launch(lambda *a: 1, torch.device("cuda", 0))
+
+
+def test_a_stream_of_a_cpu_tensor_is_refused():
+    """Calls that check nothing else of a workspace must not hand a host address to the library."""
+    import torch
+
+    ws = torch.zeros(256, dtype=torch.uint8)
+    for call in (lambda: stm._stream(ws.device), lambda: stm.read_device_error(ws),
+                 lambda: stm.selftest_wait_timeout(ws), lambda: stm.new_workspace(stm.Problem(4, 32, 4, 2, 32), "cpu")):
+        with pytest.raises(ValueError):
+            call()
