@@ -137,6 +137,7 @@ def _check(status: int) -> None:
 
 @dataclass(frozen=True)
 class Problem:
+    __slots__ = ("_c", "__dict__", "__weakref__")
     T: int
     H: int
     E: int
@@ -161,11 +162,15 @@ class Problem:
                            SHARED_KINDS[self.shared], 0)
 
     def _struct(self) -> moe_problem:
-        """c(), made once for calls that only read it."""
-        s = self.__dict__.get("_c")
-        if s is None:
-            s = self.__dict__["_c"] = self.c()
-        return s
+        """c(), made once for calls that only read it. Held in a slot: the fields alone are in vars() and in copies."""
+        try:
+            return self._c
+        except AttributeError:
+            object.__setattr__(self, "_c", self.c())
+            return self._c
+
+    def __getstate__(self):
+        return dict(self.__dict__)
 
     @property
     def torch_dtype(self) -> torch.dtype:

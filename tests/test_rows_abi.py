@@ -96,3 +96,22 @@ def test_a_stream_of_a_cpu_tensor_is_refused():
                  lambda: stm.selftest_wait_timeout(ws), lambda: stm.new_workspace(stm.Problem(4, 32, 4, 2, 32), "cpu")):
         with pytest.raises(ValueError):
             call()
+
+
+def test_a_problem_keeps_its_fields_only():
+    """The C struct that the calls keep with a problem shows neither in vars() nor in copies."""
+    import copy
+    import dataclasses
+    import json
+    import pickle
+    import weakref
+
+    p = stm.Problem(T=64, H=256, E=8, k=2, I=128, shared="plain", I_shared=64)
+    fields = dict(vars(p))
+    assert bytes(p._struct()) == bytes(p.c()) and p._struct() is p._struct()
+    assert vars(p) == fields and list(fields) == [f.name for f in dataclasses.fields(p)]
+    assert stm.Problem(**vars(p)) == p and json.loads(json.dumps(vars(p))) == fields
+    for q in (copy.copy(p), copy.deepcopy(p), pickle.loads(pickle.dumps(p)), dataclasses.replace(p)):
+        assert q == p and hash(q) == hash(p) and vars(q) == fields and bytes(q._struct()) == bytes(p.c())
+    q = dataclasses.replace(p, T=3)
+    assert q._struct().T == 3 and p._struct().T == 64 and weakref.ref(p)() is p
