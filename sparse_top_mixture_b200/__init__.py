@@ -474,6 +474,11 @@ class SparseMoE:
         self.ws = new_workspace(p, self.device)
         self.aux = torch.cuda.Stream(self.device) if (overlap_shared and p.shared != "none") else None
 
+    def _another(self) -> "SparseMoE":
+        """A layer of the same problem and weights with a workspace of its own. (Not type(self)(...): a subclass may
+        be built from other arguments.)"""
+        return SparseMoE(self.p, self.w, self.device, overlap_shared=self.aux is not None)
+
     def _outputs(self, x, out, routing_weights, selected_experts):
         p = self.p
         _req(x, "x", (p.T, p.H), p.torch_dtype)
@@ -631,7 +636,7 @@ class HostPipeline:
         self.moe = moe
         self.slots = []
         for i in range(depth):
-            m = moe if i == 0 else type(moe)(p, moe.w, moe.device, overlap_shared=moe.aux is not None)
+            m = moe if i == 0 else moe._another()
             slot = {
                 "moe": m,
                 "stream": torch.cuda.Stream(moe.device),

@@ -224,6 +224,9 @@ class Mx4SparseMoE(SparseMoE):
         if any(t is not None and t.device != self.ws.device for t in on):
             raise ValueError(f"the weights must be on {self.ws.device}")
 
+    def _another(self) -> "Mx4SparseMoE":
+        return Mx4SparseMoE(self.p, self.w, self.device)
+
     def forward(self, x, out=None, routing_weights=None, selected_experts=None, events=None):
         """out, routing_weights, selected_experts = moe(x), as SparseMoE's."""
         if events is not None:

@@ -554,6 +554,28 @@ def test_layer_in_a_graph_and_in_the_host_pipeline():
         assert torch.equal(host_out, want[0].cpu())
 
 
+@pytest.mark.parametrize("base", [stm.SparseMoE, stm.Mx4SparseMoE])
+def test_host_pipeline_of_a_subclass(base):
+    """Layers whose class is built from other arguments than a problem and weights."""
+    p, dev, moe = _layer("dsv4")
+
+    class Named(base):
+        def __init__(self, name):
+            super().__init__(p, dev)
+            self.name = name
+
+    named = Named("first")
+    pipe = stm.HostPipeline(named, depth=3)
+    assert pipe.slots[0]["moe"] is named
+    assert all(isinstance(s["moe"], base) and s["moe"].ws.data_ptr() != named.ws.data_ptr() for s in pipe.slots[1:])
+    want = named(dev["x"])[0].cpu()
+    for _ in range(3):
+        host_out = torch.empty(p.T, p.H, dtype=torch.bfloat16).pin_memory()
+        pipe.submit(dev["x"].cpu().pin_memory(), host_out)
+        pipe.synchronize()
+        assert torch.equal(host_out, want)
+
+
 def test_layer_counts_after_a_replay_are_the_replays():
     p, dev, moe = _layer("dsv4")
     x = dev["x"].clone()
