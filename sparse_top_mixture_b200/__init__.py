@@ -188,6 +188,15 @@ def _stream(device: Optional[torch.device] = None) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if index is None else index)
 
 
+def _written(*tensors: Optional[torch.Tensor]) -> None:
+    """Tells autograd that tensors of the caller's have been written: the library writes through their addresses, and
+    a graph that holds one of them (a plan, routing weights) has to refuse its backward pass then, as after any
+    in-place operation."""
+    given = [t for t in tensors if t is not None]
+    if given:
+        torch.autograd.graph.increment_version(given)
+
+
 def _launch(fn, device: torch.device, *args) -> None:
     """fn(*args, stream) on device's current stream, with device the current one."""
     index = device.index
@@ -346,6 +355,8 @@ def dispatch_noalloc(p: Problem, selected, x=None, out: Optional[Dict[str, torch
         _check(lib().moe_dispatch_noalloc(ctypes.byref(p.c()), _ptr(selected), _ptr(x), _ptr(r["counts"]),
                                           _ptr(r["offsets"]), _ptr(r["sorted_pairs"]), _ptr(r["pair_pos"]),
                                           _ptr(r["x_perm"]), _stream(dev)))
+    if out is not None:
+        _written(*(out.get(key) for key in r if r[key] is not None))
     return r
 
 
@@ -453,6 +464,8 @@ def backward(p: Problem, weights: Dict[str, Optional[torch.Tensor]], x, dout, se
     cg = moe_grads(*[_ptr(g[f]) for f, _ in moe_grads._fields_])
     _check(lib().moe_backward(ctypes.byref(p.c()), ctypes.byref(cw), _ptr(x), _ptr(dout), _ptr(selected),
                               ctypes.byref(cg), ws.data_ptr(), ws.numel(), _stream(dev)))
+    if out is not None:
+        _written(*(out.get(key) for key in g if g[key] is not None))
     return g
 
 
@@ -493,7 +506,7 @@ class SparseMoE:
         """out, routing_weights, selected_experts = moe(x). ``events``: optional
         len(STAGES)+1 torch.cuda.Event recorded before each stage and after the
         combine."""
-        p = self.p
+        p, given = self.p, (out, routing_weights, selected_experts)
         out, rw, sel = self._outputs(x, out, routing_weights, selected_experts)
         arr = None
         if events is not None:
@@ -503,6 +516,7 @@ class SparseMoE:
         aux = self.aux.cuda_stream if self.aux is not None else None
         _check(lib().moe_forward_ex(ctypes.byref(p.c()), ctypes.byref(self._cw), _ptr(x), _ptr(out), _ptr(rw),
                                     _ptr(sel), self.ws.data_ptr(), self.ws.numel(), _stream(x.device), aux, arr))
+        _written(*given)
         return out, rw, sel
 
     __call__ = forward
@@ -536,6 +550,7 @@ def bias_stash(p: Problem, counts: torch.Tensor, load_stash: torch.Tensor) -> No
     _req(counts, "counts", (p.E,), torch.int32)
     _req(load_stash, "load_stash", (p.E,), torch.int64)
     _check(lib().moe_bias_stash(ctypes.byref(p.c()), _ptr(counts), _ptr(load_stash), _stream(counts.device)))
+    _written(load_stash)
 
 
 def bias_update(p: Problem, load_stash: torch.Tensor, bias: torch.Tensor, rate: float) -> None:
@@ -545,6 +560,7 @@ def bias_update(p: Problem, load_stash: torch.Tensor, bias: torch.Tensor, rate: 
     _req(bias, "bias", (p.E,), torch.float32)
     _check(lib().moe_bias_update(ctypes.byref(p.c()), _ptr(load_stash), _ptr(bias), float(rate),
                                  _stream(bias.device)))
+    _written(load_stash, bias)
 
 
 def allreduce_loads(load_stash: torch.Tensor, group=None) -> torch.Tensor:
@@ -613,6 +629,7 @@ class GraphedForward:
 
     def replay(self):
         self.graph.replay()
+        _written(self.out, self.rw, self.sel)
         return self.out, self.rw, self.sel
 
     __call__ = replay

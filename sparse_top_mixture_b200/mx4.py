@@ -22,7 +22,7 @@ from typing import Dict, NamedTuple, Optional, Sequence, Tuple
 
 import torch
 
-from . import DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, lib, new_workspace
+from . import DTYPES, TORCH_DTYPE, Problem, SparseMoE, _launch, _ptr, _req, _written, lib, new_workspace
 from .rows import _plan, _req_at
 
 _DTYPE_ID = {TORCH_DTYPE[name]: i for name, i in DTYPES.items()}
@@ -232,6 +232,7 @@ class Mx4SparseMoE(SparseMoE):
         if events is not None:
             raise ValueError("stage events are recorded by SparseMoE only")
         p, w, ws = self.p, self.w, self.ws
+        given = (out, routing_weights, selected_experts)
         out, rw, sel = self._outputs(x, out, routing_weights, selected_experts)
         dev = ws.device
         _req_at(x, "x", (p.T, p.H), torch.bfloat16, dev.index)
@@ -257,6 +258,7 @@ class Mx4SparseMoE(SparseMoE):
                     w["shared_down"].data_ptr(), _ptr(gamma), shared.data_ptr(), ws.data_ptr(), ws.numel())
         _launch(lib().moe_unpermute_rows, dev, p._struct(), DTYPES["bf16"], y.data_ptr(), pos.data_ptr(), rw.data_ptr(),
                 _ptr(shared), out.data_ptr())
+        _written(*given)
         return out, rw, sel
 
     __call__ = forward

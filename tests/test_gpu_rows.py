@@ -383,6 +383,46 @@ def test_forward_mode_is_refused():
             torch.func.jvp(call, (t,), (torch.ones_like(t),))
 
 
+def _loss(p, plan, w, y_dtype=torch.bfloat16):
+    y = _rand((p.T * p.k, p.H), y_dtype, 1).cuda().requires_grad_(True)
+    return stm.unpermute_rows(p, y, plan, w).float().sum()
+
+
+def test_a_plan_that_is_overwritten_before_the_backward_pass():
+    """The library writes given buffers through their addresses; autograd has to know."""
+    p = _problem((12, 32, 4, 2))
+    sel = torch.rand(p.T, p.E, device="cuda").topk(p.k, 1).indices
+    plan = stm.dispatch_noalloc(p, sel)
+    w = torch.rand(p.T, p.k, device="cuda", requires_grad=True)
+    x = _rand((p.T, p.H), torch.bfloat16, 1).cuda().requires_grad_(True)
+    for loss in (lambda: _loss(p, plan, w), lambda: stm.permute_rows(p, x, plan).float().sum()):
+        loss().backward()  # a plan that stays: nothing to refuse
+        late = loss()
+        again = stm.dispatch_noalloc(p, sel.flip(0).contiguous(), out=plan)
+        assert again["pair_pos"] is plan["pair_pos"]
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            late.backward()
+
+
+@pytest.mark.parametrize("kind", ["SparseMoE", "Mx4SparseMoE", "graph"])
+def test_routing_weights_that_are_overwritten_before_the_backward_pass(kind):
+    p = stm.Problem(T=12, H=64, E=4, k=2, I=32)
+    g = torch.Generator().manual_seed(0)
+    dev = {name: torch.randn(*s, generator=g).bfloat16().cuda()
+           for name, s in (("gate_w", (4, 64)), ("gate_up", (4, 64, 64)), ("down", (4, 64, 32)))}
+    moe = (stm.Mx4SparseMoE if kind == "Mx4SparseMoE" else stm.SparseMoE)(p, dev)
+    x = _rand((p.T, p.H), torch.bfloat16, 1).cuda()
+    rw, sel = torch.empty(p.T, p.k, device="cuda"), torch.empty(p.T, p.k, dtype=torch.int64, device="cuda")
+    run = stm.GraphedForward(moe, x, None, rw, sel) if kind == "graph" else lambda: moe(x, None, rw, sel)
+    run()
+    plan = stm.dispatch(p, sel)
+    _loss(p, plan, rw).backward()
+    late = _loss(p, plan, rw)
+    run()
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        late.backward()
+
+
 def test_refusals():
     p = _problem((4, 32, 4, 2))
     _, plan = _plan(p, 0.0)
