@@ -343,22 +343,28 @@ __device__ __forceinline__ Tile decode(const Ctl* ctl, int E, int units, int n_t
   return t;
 }
 
-// silu(g) = g / (1 + 2^(-g log2 e)). The product with log2 e is carried in two
-// parts (its rounding would grow with |g|); clamping g to +-88 there keeps
-// 1 + 2^t finite and changes silu by less than 2^-119 |g|. Off by at most 2^-21
-// of the value. (Division and expf cost a slow path on zeros and tiny values,
-// which the rows past a segment hold: 60 thousand clocks a tile.)
+// silu(g) = g / (1 + 2^u), u = -g log2 e. u / 2 is carried in two parts (its
+// rounding would grow with |g|), and 2^u is the square of 2^(u/2). All of the
+// denominator is taken times 2^-64, so that neither it nor its reciprocal leaves
+// the normal numbers before silu itself does: for g in [-131, 3e38] off by at
+// most 2^-20 of the value (2^-21 from the squared ex2.approx, the rest from
+// rcp.approx and three products) and, where 1 / (1 + 2^u) is below 2^-126, by
+// 2^-150 |g|. Below -131, where silu is less than 2^-180, the reciprocal is 0,
+// and so is the result; for -inf it is NaN as in the quotient. (Division and expf
+// cost a slow path on zeros and tiny values, which the rows past a segment hold:
+// 60 thousand clocks a tile.)
 __device__ __forceinline__ float silu(float g) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  constexpr float kLog2eLow = (float)(1.4426950408889634074 - (double)kLog2e);
-  const float x = -fminf(fmaxf(g, -88.f), 88.f);
-  const float t = x * kLog2e;
-  const float low = fmaf(x, kLog2eLow, fmaf(x, kLog2e, -t));
+  constexpr float kHalfLog2e = 0.5f * 1.4426950408889634f;
+  constexpr float kHalfLog2eLow = (float)(0.5 * 1.4426950408889634074 - (double)kHalfLog2e);
+  constexpr float kTiny = 0x1p-64f;
+  const float x = -fminf(fmaxf(g, -133.f), 88.f);
+  const float t = x * kHalfLog2e;
+  const float low = fmaf(x, kHalfLog2eLow, fmaf(x, kHalfLog2e, -t));
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
   e = fmaf(e, low * 0.6931471805599453f, e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return g * r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e * kTiny, e, kTiny)));
+  return g * (r * kTiny);
 }
 
 // A warp stages boxes of its 32 rows by BYTES (64 or 128) of a row and stores

@@ -325,6 +325,34 @@ def test_swiglu_far_from_zero():
         assert bool(((got - ref).abs() <= (2.0 ** -8 + 2.0 ** -20) * ref.abs() + 2.0 ** -119 * q.abs() + 2.0 ** -133).all()), gate
 
 
+def test_swiglu_where_the_gate_almost_vanishes():
+    """Gates so negative that 1 / (1 + e^-g) is subnormal in fp32 while silu(g), or its product with a large up value,
+    is not. Off by 2^-20 of the value (see above) and by half a subnormal step of the sigmoid, 2^-150, times |g|; the
+    product is rounded to bf16."""
+    gates = torch.tensor([-80.0, -86.5, -87.0, -87.25, -87.5, -88.0, -88.5, -88.75, -89.0, -90.0, -92.5, -95.0, -97.25,
+                          -100.0, -104.0, -110.5, -112.0, -120.5, -127.0, -130.0, -131.0, -132.0, -133.0, -133.5, -140.0,
+                          -200.0, 0.5, 87.5, 88.5, 100.0, 133.5, 200.0], dtype=torch.float64)
+    # row 0 of A has a one in the first place of each block of 32, and W's row n the bits of gate n, one to a block
+    I, bits = 32, [2.0 ** i for i in range(7, -3, -1)]
+    K = 32 * len(bits)
+    x, wt = torch.zeros(1, K), torch.zeros(1, 2 * I, K)
+    x[0, ::32] = 1.0
+    for n, gate in enumerate(gates.tolist()):
+        left = abs(gate)
+        for i, bit in enumerate(bits):
+            if left >= bit:
+                wt[0, n, 32 * i] = bit if gate > 0 else -bit
+                left -= bit
+        assert left == 0
+    off = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    for up in (1.0, 2.0 ** 60, 2.0 ** 100, 2.0 ** 118):
+        wt[0, I:, 0] = up
+        got = stm.mx4_grouped_gate_up(stm.mx4_quantize(x.cuda()), stm.mx4_quantize(wt.cuda()), off)[0].double().cpu()
+        ref = gates * torch.sigmoid(gates) * up
+        bound = (2.0 ** -8 + 2.0 ** -20) * ref.abs() + 2.0 ** -150 * gates.abs() * up + 2.0 ** -133
+        assert bool(((got - ref).abs() <= bound).all()), gates[(got - ref).abs() > bound]
+
+
 def test_two_products_at_once_and_replayed():
     """Two streams that run products of different sizes at the same time, and the same from graphs that share a
     workspace."""
