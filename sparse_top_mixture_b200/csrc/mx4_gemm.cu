@@ -565,7 +565,6 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       commit<PAIR>(smem_u32(&ctl->drain));
       mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     }
-    if (PAIR && !leader) mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- scales from shared memory to TMEM ----------------
@@ -612,7 +611,6 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       commit<PAIR>(smem_u32(&ctl->cdrain));
       mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
     }
-    if (PAIR && !leader) mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
     __syncwarp();
   } else if (warp < EPI_WARP0) {
     // ---------------- scale producers ----------------
@@ -813,7 +811,18 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
 
   tc_fence_before();
   __syncthreads();
-  if constexpr (PAIR) cluster_sync_all();  // no remote arrive or pair MMA still targets either CTA
+  if constexpr (PAIR) {
+    // The leader's last commits arrive in the second CTA too. (It waits for them here, where they are due, and not
+    // from its start on: a wait is shorter than a large product.)
+    if (!leader && warp == 1) {
+      if (lane == 0) {
+        mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
+        mbar_wait(&ctl->cdrain, 0, &ctl->abort, args.err, 7, true);
+      }
+      __syncwarp();
+    }
+    cluster_sync_all();  // no remote arrive or pair MMA still targets either CTA
+  }
   tc_fence_after();
   if (warp == 1) {
     __syncwarp();

@@ -353,6 +353,29 @@ def test_swiglu_where_the_gate_almost_vanishes():
         assert bool(((got - ref).abs() <= bound).all()), gates[(got - ref).abs() > bound]
 
 
+def test_a_product_longer_than_a_wait():
+    """A launch of pairs that runs for seconds, longer than any one of its bounded waits. Codes with scales of 1 are
+    multiples of 1/2, and a sum of 393216 of their products (at most 36 each, of either sign) stays far below 2^22, so
+    that fp32 holds every partial sum exactly."""
+    rows, N, K = 98304, 98304, 393216
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def codes(*lead):
+        return stm.Mx4(torch.randint(0, 256, (*lead, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+                       torch.full((*lead, K // 32), 127, dtype=torch.uint8, device="cuda"))
+
+    a, w = codes(rows), codes(1, N)
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    y = stm.mx4_grouped_matmul(a, w, off, ws=ws)
+    assert stm.read_device_error(ws) == 0
+    i = torch.cat((torch.arange(0, rows, 1531), torch.arange(rows - 256, rows, 5))).cuda()
+    j = torch.cat((torch.arange(0, N, 769), torch.arange(N - 200, N, 7))).cuda()
+    ref = ref_values(stm.Mx4(a.data[i], a.scale[i])) @ ref_values(stm.Mx4(w.data[0, j], w.scale[0, j])).T
+    assert float(ref.abs().max()) < 2 ** 20
+    assert torch.equal(y[i][:, j], ref.to(torch.bfloat16))
+
+
 def test_two_products_at_once_and_replayed():
     """Two streams that run products of different sizes at the same time, and the same from graphs that share a
     workspace."""
