@@ -37,7 +37,8 @@
 // row tiles, known to the device only (choose_units); the ring's stages follow.
 // For large segments two CTAs share a tile of 256 rows by 3 units: each loads
 // its own rows of A and half of W's, and the leader's threads issue the MMAs
-// and scale copies of both (use_pairs says when).
+// and scale copies of both (use_pairs says when); the second CTA's warp 1 tells the
+// leader of its scales (forward_scales), its warp 2 idles.
 //
 // Waits are bounded as in gemm_tc.cu.
 #include <cuda.h>
@@ -70,9 +71,9 @@ constexpr int ACC_COLS = MAX_UNITS * UNIT;         // TMEM columns of one accumu
 constexpr int SF_COL = 2 * ACC_COLS;               // the stages' scale columns follow: two atoms of A, two of B
 constexpr int SFB_COL = 2 * 4;
 constexpr int TMEM_COLS = 512;
-constexpr int SF_STAGES = 4;                       // one for each scale warp
+constexpr int SF_WARPS = 4;
 constexpr int SF_WARP0 = 3;
-constexpr int EPI_WARP0 = SF_WARP0 + SF_STAGES;
+constexpr int EPI_WARP0 = SF_WARP0 + SF_WARPS;
 constexpr int GTHREADS = 32 * (EPI_WARP0 + 8);
 constexpr int STAGING_BYTES = 32 * 128;            // per epilogue warp
 
@@ -91,7 +92,17 @@ static_assert(SF_COL + ring_stages(2, false) * sf_cols(2) <= TMEM_COLS, "accumul
 static_assert(SF_COL + ring_stages(3, false) * sf_cols(3) <= TMEM_COLS, "accumulators and scales fit TMEM");
 static_assert(SF_COL + ring_stages(3, true) * sf_cols(3) <= TMEM_COLS, "accumulators and scales fit TMEM");
 __host__ __device__ constexpr int sf_stage_bytes(int units) { return 4 * (1 + sfb_blocks(units)) * SF_ATOM_BYTES; }
-constexpr int SF_RING_BYTES = SF_STAGES * sf_stage_bytes(3);
+constexpr int SF_RING_BYTES = SF_WARPS * sf_stage_bytes(MAX_UNITS);
+// Scale stages: one for each scale warp; of a pair, whose second CTA tells of a
+// stage by way of another thread, as many as fit behind its operand ring.
+__host__ __device__ constexpr int sf_ring_at(bool pair) {
+  return pair ? ring_stages(MAX_UNITS, true) * stage_bytes(MAX_UNITS, true) : RING_BYTES;
+}
+__host__ __device__ constexpr int sf_stages(bool pair) {
+  return pair ? (RING_BYTES + SF_RING_BYTES - sf_ring_at(true)) / sf_stage_bytes(MAX_UNITS) : SF_WARPS;
+}
+constexpr int MAX_SF_STAGES = sf_stages(true);
+static_assert(MAX_SF_STAGES >= SF_WARPS && sf_ring_at(true) % 1024 == 0, "a pair's scale stages");
 
 enum { OUT_BF16 = 0, OUT_F32 = 1, SWIGLU_BF16 = 2, SWIGLU_MX4 = 3 };
 constexpr bool is_swiglu(int mode) { return mode >= SWIGLU_BF16; }
@@ -123,8 +134,9 @@ struct Args {
 struct __align__(8) Ctl {
   uint64_t full[MAX_STAGES];
   uint64_t empty[MAX_STAGES];
-  uint64_t sfull[SF_STAGES];
-  uint64_t sempty[SF_STAGES];
+  uint64_t sfull[MAX_SF_STAGES];
+  uint64_t sempty[MAX_SF_STAGES];
+  uint64_t sready[MAX_SF_STAGES];  // of a pair's second CTA: its own stage is written
   uint64_t tfull[2];
   uint64_t tempty[2];
   uint64_t drain;   // every MMA is done, and every copy of scales
@@ -262,6 +274,19 @@ __device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
+// The same acquiring at cluster scope.
+__device__ __forceinline__ bool bar_test_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
       "selp.u32 %0, 1, 0, p;\n\t}\n"
       : "=r"(done)
       : "r"(bar), "r"(parity)
@@ -409,12 +434,41 @@ __device__ __forceinline__ void box_free(int lane) {
   __syncwarp();
 }
 
+// A pair's leader issues the copies of both CTAs' scale words. Those of the second
+// CTA are ordered before its copies by this thread of the second CTA: it waits for
+// the storing warp's arrive (CTA scope), and one release at cluster scope, about
+// 1500 clocks, tells the leader of every stage that is ready by then; a stage takes
+// 768. (gate_up of 8192 tokens: a release a stage by the storing warps 762 us, by
+// this thread 505, by two threads 424; several stages a release 416, as without
+// any release. The product of the same sizes: 230, without a release 225.)
+__device__ __forceinline__ void forward_scales(Ctl* ctl, int64_t vectors, int32_t* err) {
+  constexpr int kStages = sf_stages(true);
+  const uint32_t sready = smem_u32(ctl->sready), sfull = mapa_shared(smem_u32(ctl->sfull), 0);
+  Ring at{0, 0};
+  for (int64_t v = 0; v < vectors;) {
+    if (!bar_wait(sready + at.bar, at.phase, &ctl->abort, err, 11)) break;
+    Ring told = at;
+    int n = 0;
+    do {
+      ++n;
+      ++v;
+      at = at.next(8 * kStages);
+    } while (n < kStages && v < vectors && bar_test(sready + at.bar, at.phase));
+    fence_cluster();
+    for (; n > 0; --n) {
+      mbar_arrive_remote_relaxed(sfull + told.bar);
+      told = told.next(8 * kStages);
+    }
+  }
+}
+
 template <int MODE, bool PAIR>
 __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* sf_base = base + RING_BYTES;
-  uint8_t* staging = sf_base + SF_RING_BYTES;
+  constexpr int SF_STAGES = sf_stages(PAIR);
+  uint8_t* sf_base = base + sf_ring_at(PAIR);
+  uint8_t* staging = base + RING_BYTES + SF_RING_BYTES;
   Ctl* ctl = reinterpret_cast<Ctl*>(staging + 8 * STAGING_BYTES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -429,8 +483,9 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       mbar_init(&ctl->empty[s], 1);
     }
     for (int s = 0; s < SF_STAGES; ++s) {
-      mbar_init(&ctl->sfull[s], PAIR ? 2 : 1);  // a scale warp, of a pair's both CTAs
+      mbar_init(&ctl->sfull[s], PAIR ? 2 : 1);  // a scale warp, and of a pair the second CTA's forwarder
       mbar_init(&ctl->sempty[s], 1);
+      if constexpr (PAIR) mbar_init(&ctl->sready[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&ctl->tfull[a], 1);
@@ -464,6 +519,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
   const int n_tiles = (args.n_units + units - 1) / units;
   const int total = ctl->pre[args.E] * n_tiles;
   const int blocks = sfb_blocks(units);
+  // 512-value vectors of scales over this worker's tiles
+  const int64_t vectors = total > worker ? (int64_t)((total - worker - 1) / workers + 1) * ((args.k_steps + 1) / 2) : 0;
 
   if (warp == 0) {
     // ---------------- TMA producer ----------------
@@ -565,6 +622,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       commit<PAIR>(smem_u32(&ctl->drain));
       mbar_wait(&ctl->drain, 0, &ctl->abort, args.err, 7, true);
     }
+    if (PAIR && !leader && elect_one()) forward_scales(ctl, vectors, args.err);
     __syncwarp();
   } else if (warp == 2) {
     // ---------------- scales from shared memory to TMEM ----------------
@@ -584,7 +642,8 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       for (int tile = worker; ok && tile < total; tile += workers) {
         for (int kt = 0; kt < args.k_steps; ++kt) {
           ok = bar_wait(empty + at.bar, at.phase ^ 1u, &ctl->abort, args.err, 9) &&
-               ((kt & 1) || bar_wait(sfull + sf.bar, sf.phase, &ctl->abort, args.err, 10));
+               ((kt & 1) || (bar_wait(sfull + sf.bar, sf.phase, &ctl->abort, args.err, 10) &&
+                             (!PAIR || bar_test_cluster(sfull + sf.bar, sf.phase))));
           if (!ok) break;
           tc_fence_after();
           // the step's two atoms of A, and of B after A's four
@@ -614,12 +673,11 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
     __syncwarp();
   } else if (warp < EPI_WARP0) {
     // ---------------- scale producers ----------------
-    // The warps take the 512-value vectors of the CTA's tiles in turn, each into
-    // a stage of its own, so that the loads of several are in flight.
+    // The warps take the 512-value vectors of the CTA's tiles in turn, so that the
+    // loads of several are in flight.
     constexpr int kA = BM / 32, kB = MAX_UNITS * UNIT / 32;  // rows of a lane
-    const int n_vec = (args.k_steps + 1) / 2, stage = warp - SF_WARP0;
-    uint8_t* const stage_base = sf_base + stage * sf_stage_bytes(units) + lane * 16;
-    int tile = worker, kv = stage, e = 0;
+    const int n_vec = (args.k_steps + 1) / 2;
+    int tile = worker, stage = warp - SF_WARP0, kv = stage, e = 0;
     uint32_t phase = 0;
     const uint4 *src_a[kA], *src_b[kB];  // this lane's rows' scales, nullptr for a row that the tile lacks
     for (bool set_up = true;;) {
@@ -654,6 +712,7 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
 #pragma unroll
       for (int c = 0; c < kB; ++c) vb[c] = src_b[c] ? __ldg(src_b[c] + kv) : make_uint4(0, 0, 0, 0);
       if (!warp_wait(&ctl->sempty[stage], phase ^ 1u, &ctl->abort, args.err, 5)) break;
+      uint8_t* const stage_base = sf_base + stage * sf_stage_bytes(units) + lane * 16;
 #pragma unroll
       for (int atom = 0; atom < 4; ++atom) {
         // bytes past K / 32 are the caller's padding and count as zeros: the last MMA may take in one
@@ -677,14 +736,14 @@ __device__ __forceinline__ void mx4_gemm(const Maps& maps, const Args& args) {
       fence_to_async();
       __syncwarp();
       if (lane == 0) {
-        // To a pair's leader without a release at cluster scope: the fences have
-        // put the stores where the leader's copy of this CTA's memory reads, and
-        // such a release would wait about 1000 clocks for loads in flight.
-        if constexpr (PAIR) mbar_arrive_remote(mapa_shared(smem_u32(&ctl->sfull[stage]), 0));
-        else mbar_arrive(&ctl->sfull[stage]);
+        mbar_arrive(PAIR && !leader ? &ctl->sready[stage] : &ctl->sfull[stage]);
       }
-      kv += SF_STAGES;
-      phase ^= 1u;
+      kv += SF_WARPS;
+      stage += SF_WARPS;
+      if (stage >= SF_STAGES) {
+        stage -= SF_STAGES;
+        phase ^= 1u;
+      }
     }
     __syncwarp();
   } else {

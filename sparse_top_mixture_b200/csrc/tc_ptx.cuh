@@ -249,6 +249,13 @@ __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
+// An arrive that orders nothing by itself, after fence_cluster().
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+
 // TMA tile loads into this CTA's shared memory that complete transactions on
 // the mbarrier at `bar_cluster` (the pair leader's barrier).
 __device__ __forceinline__ void tma2_load_2d(void* dst, const CUtensorMap* map, uint32_t bar_cluster, int c0,

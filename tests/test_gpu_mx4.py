@@ -376,6 +376,35 @@ def test_a_product_longer_than_a_wait():
     assert torch.equal(y[i][:, j], ref.to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("gate_up", [False, True])
+def test_a_pair_uses_the_scales_of_its_own_rows(gate_up):
+    """Scales that change in every block, from launch to launch and stage to stage: a word that a CTA of a pair copied
+    before it was written would show. Codes (multiples of 1/2 up to 6) and scales of 1, 2 and 4 make every partial sum
+    of 4096 products a multiple of 1/4 below 4096 * 36 * 16 < 2^22: exact in fp32 in any order."""
+    rows, N, K = 4096, 4096, 4096
+    off = torch.tensor([0, rows], dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(3)
+    a = stm.Mx4(torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+                torch.empty(rows, K // 32, dtype=torch.uint8, device="cuda"))
+    w = stm.Mx4(torch.randint(0, 256, (1, N, K // 2), dtype=torch.uint8, device="cuda", generator=g),
+                torch.empty(1, N, K // 32, dtype=torch.uint8, device="cuda"))
+    for _ in range(6):
+        for q in (a, w):
+            q.scale.copy_(torch.randint(127, 130, q.scale.shape, dtype=torch.uint8, device="cuda", generator=g))
+        ref = ref_values(a) @ ref_values(w)[0].T
+        if gate_up:  # SwiGLU of exact gates and ups
+            gate, up = ref.chunk(2, 1)
+            ref = gate * torch.sigmoid(gate) * up
+            # besides the roundings, half a subnormal step of the sigmoid (2^-150) times gate and up: at gate -104, up
+            # 11240 that is 2^-150 * 1168960 = 8.2e-40, more than 2^-130 = 7.3e-40
+            bound = (2.0 ** -8 + 2.0 ** -19) * ref.abs() + 2.0 ** -150 * gate.abs() * up.abs() + 2.0 ** -133
+            for _ in range(4):
+                assert bool(((stm.mx4_grouped_gate_up(a, w, off).double() - ref).abs() <= bound).all())
+        else:
+            for _ in range(4):
+                assert torch.equal(stm.mx4_grouped_matmul(a, w, off, torch.float32).double(), ref)
+
+
 def test_two_products_at_once_and_replayed():
     """Two streams that run products of different sizes at the same time, and the same from graphs that share a
     workspace."""
