@@ -369,7 +369,8 @@ __device__ __forceinline__ Tile decode(const Ctl* ctl, int E, int units, int n_t
 }
 
 // silu(g) = g / (1 + 2^u), u = -g log2 e. u / 2 is carried in two parts (its
-// rounding would grow with |g|), and 2^u is the square of 2^(u/2). All of the
+// rounding would grow with |g|), t and low, and 2^u is the square of 2^t times
+// 1 + 2 low ln 2 (low is below 2^-17, its square out of reach). All of the
 // denominator is taken times 2^-64, so that neither it nor its reciprocal leaves
 // the normal numbers before silu itself does: for g in [-131, 3e38] off by at
 // most 2^-20 of the value (2^-21 from the squared ex2.approx, the rest from
@@ -385,10 +386,10 @@ __device__ __forceinline__ float silu(float g) {
   const float x = -fminf(fmaxf(g, -133.f), 88.f);
   const float t = x * kHalfLog2e;
   const float low = fmaf(x, kHalfLog2eLow, fmaf(x, kHalfLog2e, -t));
+  const float scale = fmaf(low, 2.f * 0.6931471805599453f * kTiny, kTiny);  // 2^-64 (2^low)^2
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-  e = fmaf(e, low * 0.6931471805599453f, e);
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e * kTiny, e, kTiny)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(fmaf(e * scale, e, kTiny)));
   return g * (r * kTiny);
 }
 
