@@ -18,8 +18,9 @@
 // registers, and only its k sorted rows are touched besides it, each with
 // 16-byte accesses that cover whole lines. What reaches the memory's rate is
 // the loads in flight, so the kernels are compiled for each k up to 8 (more
-// slots go eight at a time), and a thread issues those of several vectors of
-// its token before it uses the first: 8 for k 1, 4 for k 2 and 3, else 2.
+// slots go eight at a time), and a thread takes several vectors of its token at
+// once: 8 for k 1, 4 for k 2 and 3 (fp32 rows: to 5), else 2. The compiler issues
+// their loads ahead as far as its registers go.
 // (8192 x 8192 bf16, k 2: unpermute 130 us with one vector a thread, 64 with
 // four.)
 #include <cuda_runtime.h>
@@ -353,8 +354,14 @@ moe_status check_problem(const moe_problem* p) {
   return moe_workspace_size(p, &bytes);  // validates the problem
 }
 
-// Vectors of a token that a thread takes at once for SL slots.
-constexpr int vectors_for(int SL) { return SL == 1 ? 8 : SL <= 3 ? 4 : 2; }
+// Vectors of a token that a thread takes at once for SL slots of rows with
+// `bytes` an element. Of fp32 rows, whose vectors have half the values to sum,
+// four up to five slots (unpermute of 8192 x 4096 into bf16, us with four and two:
+// k 4 96 / 110; 8192 x 2048, k 5 in fp32 69 / 80, into bf16 57 / 54) and two from
+// six on (8192 x 4096, k 6, with shared_out, four and two: 171 / 160; 8192 x 2048,
+// k 7: 90 / 81); two or three slots with eight: 94 and 115, with four 84 and 111
+// (8192 x 4096, shared_out).
+constexpr int vectors_for(int SL, int bytes) { return SL == 1 ? 8 : SL <= (bytes == 4 ? 5 : 3) ? 4 : 2; }
 
 // Several vectors a thread once that leaves 512 threads for each of 148 SMs:
 // few tokens need the threads more (300 tokens of 2048 bf16, k 6: 4.6 us with
@@ -394,9 +401,7 @@ cudaError_t launch_unpermute(const void* ys, const int32_t* pair_pos, const floa
                              void* out, int64_t T, int64_t H, int64_t k, cudaStream_t s) {
   const int64_t nvec = H * sizeof(TY) / 16;
   with_slots(k, [&](auto slots) {
-    // twice as many of fp32, whose vectors have half the values to sum
-    constexpr int SL = decltype(slots)::value;
-    constexpr int V = vectors_for(SL) * (sizeof(TY) == 4 && SL > 1 && SL < kSlots ? 2 : 1);
+    constexpr int SL = decltype(slots)::value, V = vectors_for(SL, sizeof(TY));
     auto launch = [&](auto kernel, int per_thread) {
       const int64_t passes = ceil_div(nvec, per_thread);
       const int lg = lane_log2(passes);
@@ -416,7 +421,7 @@ cudaError_t launch_unpermute_backward(const void* dout, const void* ys, const in
   const int64_t nvec = H * sizeof(TY) / 16;
   with_slots(k, [&](auto slots) {
     // half as many where each load is answered by a store
-    constexpr int SL = decltype(slots)::value, V = std::max(2, vectors_for(SL) / 2);
+    constexpr int SL = decltype(slots)::value, V = std::max(2, vectors_for(SL, 2) / 2);
     auto launch = [&](auto kernel, int per_thread) {
       // A warp per token, or for short rows less (8 lanes at least: a lane
       // writes each slot's weight gradient); more for few tokens, as long as
