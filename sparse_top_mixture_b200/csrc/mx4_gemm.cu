@@ -13,9 +13,9 @@
 // of 16 tokens, 256 experts, H 7168, I 2048: 1.6 GB in 242 us, 6.6 TB/s). Many
 // rows: shared memory, which takes the operands from L2 and gives them to the
 // tensor cores (at N 192 and 256 values of K, 28 KB in and some 40 KB out a
-// step of 384 MMA clocks, 128 bytes a clock), and the power limit, which holds
-// the SM clock near 1.5 GHz (gate_up of 8192 tokens, 64 experts, H 4096, I 2048:
-// 410 us, 4.0 PFLOP/s).
+// step of 384 MMA clocks, 128 bytes a clock), and the power limit (gate_up of 8192
+// tokens, 64 experts, H 4096, I 2048: 416 us, 4.0 PFLOP/s, at 1.6 GHz in launches
+// with pauses; 469 us, 3.5 PFLOP/s, at 1.3 GHz in calls back to back for seconds).
 //
 // Design (a CTA on each SM, persistent, warp-specialised, 480 threads):
 //   warp 0      TMA producer, 256 values of K a step: the tile's rows of A (one
@@ -441,7 +441,8 @@ __device__ __forceinline__ void box_free(int lane) {
 // 1500 clocks, tells the leader of every stage that is ready by then; a stage takes
 // 768. (gate_up of 8192 tokens: a release a stage by the storing warps 762 us, by
 // this thread 505, by two threads 424; several stages a release 416, as without
-// any release. The product of the same sizes: 230, without a release 225.)
+// any release. The product of the same sizes: 231, and 225 where the storing warps
+// told the leader themselves without one.)
 __device__ __forceinline__ void forward_scales(Ctl* ctl, int64_t vectors, int32_t* err) {
   constexpr int kStages = sf_stages(true);
   const uint32_t sready = smem_u32(ctl->sready), sfull = mapa_shared(smem_u32(ctl->sfull), 0);
@@ -969,10 +970,12 @@ cudaError_t launch(int64_t rows, int64_t E, int64_t N, int64_t K, const void* a_
 }
 
 // Pairs halve the traffic of W but fill 256-row tiles: they pay from about 512
-// rows an expert on (us, one CTA / pairs: 64 experts of N 4096, K 2048 at 256
-// rows each 105 / 104, at 512 170 / 165, at 1536 435 / 399; 128 experts of N
-// 2048, K 768 at 256 58 / 60, at 1536 244 / 231), and lose with few steps a
-// pair (gate_up of 16 experts, H 1024, I 512 at 768: 23.6 / 25.3).
+// rows an expert on (us, one CTA / pairs, unequal segments of 384, 512, 768 and
+// 1024 rows in the mean: product of 64 experts, N 4096, K 2048 135 / 138, 169 / 167,
+// 236 / 230, 304 / 292; of 128 experts, N 2048, K 768 70 / 73, 87 / 88, 123 / 122,
+// 159 / 157; gate_up of 64 experts, H 4096, I 2048 253 / 251, 318 / 304, 443 / 416,
+// 565 / 526), and lose with few steps a pair (gate_up of 16 experts, H 1024, I 512
+// at 768: 17.9 / 20.7).
 bool use_pairs(int64_t rows, int64_t E, int64_t n_units, int64_t k_steps) {
   return rows >= 512 * E && rows / (2 * BM) * ceil_div(n_units, MAX_UNITS) * k_steps >= 64 * (num_sms() / 2);
 }
