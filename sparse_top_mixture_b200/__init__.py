@@ -12,6 +12,7 @@ Build the library with ``python -m sparse_top_mixture_b200.build``.
 
 from __future__ import annotations
 
+import copy
 import ctypes
 import os
 from dataclasses import dataclass
@@ -488,9 +489,12 @@ class SparseMoE:
         self.aux = torch.cuda.Stream(self.device) if (overlap_shared and p.shared != "none") else None
 
     def _another(self) -> "SparseMoE":
-        """A layer of the same problem and weights with a workspace of its own. (Not type(self)(...): a subclass may
+        """The same layer with a workspace and a second stream of its own. (A copy, not type(self)(...): a subclass may
         be built from other arguments.)"""
-        return SparseMoE(self.p, self.w, self.device, overlap_shared=self.aux is not None)
+        other = copy.copy(self)
+        other.ws = new_workspace(self.p, self.device)
+        other.aux = None if self.aux is None else torch.cuda.Stream(self.device)
+        return other
 
     def _outputs(self, x, out, routing_weights, selected_experts):
         p = self.p

@@ -225,7 +225,9 @@ class Mx4SparseMoE(SparseMoE):
             raise ValueError(f"the weights must be on {self.ws.device}")
 
     def _another(self) -> "Mx4SparseMoE":
-        return Mx4SparseMoE(self.p, self.w, self.device)
+        other = super()._another()
+        other._counts = torch.zeros_like(self._counts)
+        return other
 
     def forward(self, x, out=None, routing_weights=None, selected_experts=None, events=None):
         """out, routing_weights, selected_experts = moe(x), as SparseMoE's."""

@@ -656,6 +656,34 @@ def test_host_pipeline_of_a_subclass(base):
         assert torch.equal(host_out, want)
 
 
+@pytest.mark.parametrize("base", [stm.SparseMoE, stm.Mx4SparseMoE])
+def test_host_pipeline_runs_a_subclass_in_every_slot(base):
+    """A subclass's forward, on every slot's own workspace, stream and counts."""
+    p, dev, _ = _layer("dsv4")
+
+    class Doubled(base):
+        def forward(self, x, out=None, *args, **kw):
+            out, rw, sel = super().forward(x, out, *args, **kw)
+            return out.mul_(2), rw, sel
+
+        __call__ = forward
+
+    moe = Doubled(p, dev)
+    want = moe(dev["x"])[0].cpu()
+    for graphs in (False, True):
+        pipe = stm.HostPipeline(moe, depth=3, graphs=graphs)
+        slots = [s["moe"] for s in pipe.slots]
+        for get in (lambda m: m.ws.data_ptr(), lambda m: m.forward_counts().data_ptr()):
+            assert len({get(m) for m in slots}) == 3
+        if moe.aux is not None:
+            assert len({m.aux.cuda_stream for m in slots}) == 3
+        for _ in range(3):
+            host_out = torch.empty(p.T, p.H, dtype=torch.bfloat16).pin_memory()
+            pipe.submit(dev["x"].cpu().pin_memory(), host_out)
+            pipe.synchronize()
+            assert torch.equal(host_out, want)
+
+
 def test_layer_counts_after_a_replay_are_the_replays():
     p, dev, moe = _layer("dsv4")
     x = dev["x"].clone()
