@@ -6,9 +6,9 @@ slots, ``unpermute_rows`` sums a token's k rows with the routing weights. Both
 take part in autograd (in ``x``; in ``y_perm``, ``routing_weights`` and
 ``shared_out``), once and in reverse mode: tensors with a forward-mode tangent
 are refused. Plan and routing weights must stay as they are until the backward
-pass (overwriting them makes it raise). ``permute_rows_backward`` and ``unpermute_rows_backward`` are
-their gradients as plain calls. The plan is what ``dispatch`` or
-``dispatch_slots`` returned for the same problem.
+pass (overwriting them makes it raise). ``permute_rows_backward`` and
+``unpermute_rows_backward`` are their gradients as plain calls. The plan is
+what ``dispatch`` or ``dispatch_slots`` returned for the same problem.
 
     plan = stm.dispatch(p, selected_experts)
     rows = stm.permute_rows(p, x, plan)                 # [T*k, H], by expert
